@@ -7,6 +7,9 @@
  * library computes the two backward products and then updates an fp32
  * master copy of the weights with AdamW.
  *
+ * Around that path it has the softmax cross entropy of the model's head, where
+ * the backward pass starts.
+ *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers on the current HIP device,
  *    owned by the caller; the library never allocates, frees or retains them.
@@ -37,7 +40,7 @@ extern "C" {
 /* element type of X, W, dY and dX in lin_bwd() */
 #define LB_F32 0  /* IEEE binary32 */
 #define LB_BF16 1 /* bfloat16 (upper half of a binary32) */
-#define LB_F16 2  /* IEEE binary16 (gradients and 16-bit weight copies only) */
+#define LB_F16 2  /* IEEE binary16 (gradients, 16-bit weight copies, the loss head) */
 
 /* return codes */
 #define LB_OK 0
@@ -254,6 +257,72 @@ int grad_norm(const void *grad, int grad_dtype, int64_t n, float inv_scale, floa
  * LB_EHIP when a launch fails.
  */
 int softmax_bwd(const void *P, const void *dY, void *dX, int64_t rows, int64_t cols, int dtype);
+
+/*
+ * lin_xent -- softmax cross entropy of a Linear head (the largest Linear layer
+ * of a language model, whose backward pass starts at this loss), without
+ * storing the logits:
+ *     z      = X·W                                             [M,V], never stored
+ *     lse[m] = log Σ_v exp z[m,v]
+ *     loss[m]= lse[m] − z[m, target[m]]
+ *     out[0] = mean of loss over the counted rows,  out[1] = 1 / their number
+ *
+ *   X       [M,K]  dtype   read only
+ *   W       [K,V]  dtype   read only
+ *   target  [M]    int64   device; a negative target takes its row out: loss and
+ *                          lse are 0 there and it is not counted, whatever its X
+ *                          holds.  A target >= V gives that row a NaN loss (and a
+ *                          NaN mean); nothing is read out of range.
+ *   loss, lse [M] fp32, out [2] fp32   written.  With no counted row out is 0, 0.
+ *   dtype   LB_BF16 or LB_F16 (fp32 accumulation, fp32 statistics and lse, the
+ *           mean summed in fp64, all in a fixed order: results repeat bit for bit)
+ *   ws      device memory of at least lin_xent_workspace(M, K, V) bytes, 16-byte
+ *           aligned, the caller's; it holds per-tile maxima and sums and, where V
+ *           is no multiple of 8 or W is not 16-byte aligned, a padded copy of a
+ *           piece of W.  Nothing in it is kept from call to call, and the call
+ *           allocates nothing: it may be captured into a graph, and calls that
+ *           may overlap (other streams, two graphs) take workspaces of their own.
+ *
+ * Any alignment of the elements and any K and V from 1 to 2^22 − 1; M < 2^27.
+ * M = 0 writes out = 0, 0 only.  NaN and infinity propagate to their rows.
+ * Errors: LB_EDTYPE for another dtype (fp32 operands have no MFMA path here);
+ * LB_EINVAL for a size out of range, a NULL buffer, or a workspace that is NULL,
+ * unaligned or too small; LB_EHIP when a launch fails.
+ */
+int64_t lin_xent_workspace(int64_t M, int64_t K, int64_t V);
+int lin_xent(const void *X, const void *W, const int64_t *target, float *loss, float *lse, float *out,
+             int64_t M, int64_t K, int64_t V, int dtype, void *ws, int64_t ws_bytes);
+
+/*
+ * lin_xent_bwd -- the gradients of lin_xent's loss with respect to X and W, from
+ * its lse; the logits are computed again, a piece of the vocabulary at a time:
+ *     s[m]   = scale · d_scale[0] · row_scale[m]      (0 where target[m] < 0)
+ *     G[m,v] = (exp(z[m,v] − lse[m]) − [v = target[m]]) · s[m]
+ *     dX = G·Wᵀ  [M,K]        dW = Xᵀ·G  [K,V]
+ *
+ *   X, W, target, M, K, V, dtype   as for lin_xent
+ *   lse        [M] fp32  lin_xent's
+ *   row_scale  [M] fp32  the upstream gradient of each row's loss, or NULL (1)
+ *   d_scale    device pointer to one float, or NULL (1): pass lin_xent's out + 1
+ *              for the gradient of the mean, without a host round trip
+ *   scale      a host factor: the loss scale of mixed-precision training
+ *   dX, dW     dtype     written (overwritten); NULL skips one
+ *   ws         device memory of at least lin_xent_bwd_workspace(M, K, V) bytes,
+ *              as for lin_xent; it holds a piece of G (at most about 512 MiB), a
+ *              copy of X and, over several pieces, dX's fp32 sums
+ *
+ * Rows with a negative target, or with s[m] = 0, have no gradient: their dX is 0
+ * and their X is not used, whatever it holds.  A target >= V makes its row's dX
+ * and all of dW NaN.  G is rounded once to dtype, the operand type of the two
+ * products (for LB_F16 after scaling by the power of two that brings max |s| to
+ * [2^14, 2^15), so small probabilities stay above fp16's smallest normal; taken
+ * out in fp32), dX and dW once at the end.  Results repeat bit for bit.
+ * M = 0 fills dW with zeros.  Both outputs NULL is a no-op.  Errors: lin_xent's.
+ */
+int64_t lin_xent_bwd_workspace(int64_t M, int64_t K, int64_t V);
+int lin_xent_bwd(const void *X, const void *W, const int64_t *target, const float *lse,
+                 const float *row_scale, const float *d_scale, float scale, void *dX, void *dW,
+                 int64_t M, int64_t K, int64_t V, int dtype, void *ws, int64_t ws_bytes);
 
 /*
  * lb_set_stream -- the HIP stream (a hipStream_t, passed as void*) on which

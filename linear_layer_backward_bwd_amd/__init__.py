@@ -12,7 +12,8 @@ import ctypes
 import os
 
 __all__ = ["lin_bwd", "lin_bwd_ex", "adamw_step", "adamw_step_f16", "adamw_step_bf16",
-           "adamw_step_ex", "grad_norm", "softmax_bwd", "lb_set_stream", "lb_set_lin_bwd_path",
+           "adamw_step_ex", "grad_norm", "softmax_bwd", "lin_xent", "lin_xent_bwd",
+           "lin_xent_workspace", "lin_xent_bwd_workspace", "lb_set_stream", "lb_set_lin_bwd_path",
            "lin_bwd_path", "lb_last_error", "lb_version", "lb_shutdown", "library", "LIB_PATH",
            "LB_F32", "LB_BF16", "LB_F16", "LB_PATH_AUTO", "LB_PATH_TILE", "LB_PATH_SMALL_M",
            "LB_PATH_GENERAL", "LB_PATH_FUSED_SMALL_M"]
@@ -52,6 +53,13 @@ def library() -> ctypes.CDLL:
     lib.adamw_step_ex.restype = i32
     lib.grad_norm.argtypes = [vp, i32, i64, f32, f32, vp, vp]
     lib.grad_norm.restype = i32
+    lib.lin_xent.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, i32, vp, i64]
+    lib.lin_xent.restype = i32
+    lib.lin_xent_bwd.argtypes = [vp, vp, vp, vp, vp, vp, f32, vp, vp, i64, i64, i64, i32, vp, i64]
+    lib.lin_xent_bwd.restype = i32
+    for name in ("lin_xent_workspace", "lin_xent_bwd_workspace"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = i64
     lib.lb_set_stream.argtypes = [vp]
     lib.lb_set_stream.restype = i32
     lib.lb_set_lin_bwd_path.argtypes = [i32]
@@ -341,3 +349,124 @@ def softmax_bwd(P, dY, dX=None):
                                LB_BF16 if P.dtype == torch.bfloat16 else LB_F32)
     _check(rc, "softmax_bwd")
     return dX
+
+
+class _on_device:
+    """Makes dev the current device and its current stream the library's, for one call."""
+
+    def __init__(self, dev):
+        self.dev, self.back = dev, None
+
+    def __enter__(self):
+        import torch
+        if torch.cuda.current_device() != self.dev.index:
+            self.back = torch.cuda.current_device()
+            torch.cuda.set_device(self.dev)
+        _use_current_stream(self.dev)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _workspace(ws, need, dev):
+    """The caller's workspace tensor, or one from torch's allocator (ordered on the current
+    stream, a captured graph's own while one is being captured)."""
+    import torch
+    if ws is None:
+        return torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError("ws must be contiguous and hold %d bytes" % need)
+    return ws
+
+
+def _xent_args(X, W, target, vectors):
+    import torch
+    if X.dtype not in (torch.bfloat16, torch.float16) or W.dtype != X.dtype:
+        raise TypeError("X and W must both be bfloat16 or both float16")
+    if X.dim() != 2 or W.dim() != 2 or W.shape[0] != X.shape[1]:
+        raise ValueError("X must be [M,K] and W [K,V]: X%s W%s" % (tuple(X.shape), tuple(W.shape)))
+    M, K = X.shape
+    V = W.shape[1]
+    if target.dtype != torch.int64 or tuple(target.shape) != (M,):
+        raise ValueError("target must be int64 of shape (%d,)" % M)
+    for t, nm in vectors:
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (M,)):
+            raise ValueError("%s must be float32 of shape (%d,)" % (nm, M))
+    return M, K, V, LB_BF16 if X.dtype == torch.bfloat16 else LB_F16
+
+
+def lin_xent(X, W, target, loss=None, lse=None, out=None, ws=None):
+    """Softmax cross entropy of the head X·W against target, without storing the logits
+    (C: lin_xent).
+
+    X [M,K], W [K,V]: both bfloat16 or both float16; target [M] int64, negative where a
+    row takes no part.  Returns (loss [M], lse [M], out) in float32; out = [mean loss over
+    the counted rows, 1 / their number].  Tensors may be given to reuse them; ws is device
+    memory of at least lin_xent_workspace(M, K, V) bytes, or None to take it from torch.
+    """
+    import torch
+    M, K, V, code = _xent_args(X, W, target, ((loss, "loss"), (lse, "lse")))
+    loss = torch.empty(M, dtype=torch.float32, device=X.device) if loss is None else loss
+    lse = torch.empty(M, dtype=torch.float32, device=X.device) if lse is None else lse
+    out = torch.empty(2, dtype=torch.float32, device=X.device) if out is None else out
+    if out.dtype != torch.float32 or out.numel() != 2:
+        raise TypeError("out must be a two-element float32 tensor")
+    dev = _device_of([X, W, target, loss, lse, out, ws])
+    lib = library()
+    need = lin_xent_workspace(M, K, V)
+    with _on_device(dev):
+        ws = _workspace(ws, need, dev)
+        rc = lib.lin_xent(_ptr(X), _ptr(W), _ptr(target), _ptr(loss), _ptr(lse), _ptr(out), M, K, V, code,
+                          _ptr(ws), ws.numel() * ws.element_size())
+        _check(rc, "lin_xent")
+    return loss, lse, out
+
+
+def lin_xent_bwd(X, W, target, lse, dX=None, dW=None, scale=1.0, d_scale=None, row_scale=None, ws=None) -> None:
+    """Gradients of lin_xent's loss (C: lin_xent_bwd): dX = G·Wᵀ into dX, dW = Xᵀ·G into dW,
+    both of the operands' type, with G = (softmax(X·W) − onehot(target)) · s and
+    s = scale · d_scale · row_scale per row, 0 where target is negative.
+
+    lse: lin_xent's.  d_scale: a one-element float32 GPU tensor (lin_xent's out[1:] for the
+    gradient of the mean) or None.  row_scale: float32 [M] or None.  dX or dW may be None to
+    skip it.  ws: device memory of at least lin_xent_bwd_workspace(M, K, V) bytes, or None.
+    """
+    import torch
+    M, K, V, code = _xent_args(X, W, target, ((lse, "lse"), (row_scale, "row_scale")))
+    if lse is None:
+        raise ValueError("lse is required")
+    if d_scale is not None and (d_scale.dtype != torch.float32 or d_scale.numel() != 1):
+        raise TypeError("d_scale must be a one-element float32 tensor")
+    for t, nm, shape in ((dX, "dX", (M, K)), (dW, "dW", (K, V))):
+        if t is not None and (t.dtype != X.dtype or tuple(t.shape) != shape):
+            raise ValueError("%s must be %s of shape %s" % (nm, X.dtype, shape))
+    if dX is None and dW is None:
+        return
+    dev = _device_of([X, W, target, lse, row_scale, d_scale, dX, dW, ws])
+    lib = library()
+    need = lin_xent_bwd_workspace(M, K, V)
+    with _on_device(dev):
+        ws = _workspace(ws, need, dev)
+        rc = lib.lin_xent_bwd(_ptr(X), _ptr(W), _ptr(target), _ptr(lse), _ptr(row_scale), _ptr(d_scale), scale,
+                              _ptr(dX), _ptr(dW), M, K, V, code, _ptr(ws), ws.numel() * ws.element_size())
+        _check(rc, "lin_xent_bwd")
+
+
+def _bytes(name, *sizes):
+    n = getattr(library(), name)(*sizes)
+    if n < 0:
+        _check(n, name)
+    return n
+
+
+def lin_xent_workspace(M: int, K: int, V: int) -> int:
+    """Bytes of device memory that lin_xent needs for these sizes."""
+    return _bytes("lin_xent_workspace", M, K, V)
+
+
+def lin_xent_bwd_workspace(M: int, K: int, V: int) -> int:
+    """Bytes of device memory that lin_xent_bwd needs for these sizes."""
+    return _bytes("lin_xent_bwd_workspace", M, K, V)

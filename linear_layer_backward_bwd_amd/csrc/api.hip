@@ -10,6 +10,7 @@
 
 #include "../../include/linbwd.h"
 #include "kernels.h"
+#include "plan_xent.h"
 
 namespace {
 
@@ -243,6 +244,29 @@ int adamw_impl(const char *name, lb::GradType gt, float *W, const void *g, float
     return LB_OK;
 }
 
+// lin_xent and lin_xent_bwd: sizes the kernels' descriptors and grids cover
+bool xent_sizes_ok(int64_t M, int64_t K, int64_t V) {
+    return M >= 0 && M < ((int64_t)1 << 27) && K >= 1 && K < lb::xent::kMaxWidth && V >= 1 &&
+           V < lb::xent::kMaxWidth;
+}
+
+int xent_check(const char *name, int64_t M, int64_t K, int64_t V, int dtype) {
+    if (dtype != LB_BF16 && dtype != LB_F16)
+        return fail(LB_EDTYPE, "%s: dtype %d is not LB_BF16 (1) or LB_F16 (2)", name, dtype);
+    if (!xent_sizes_ok(M, K, V))
+        return fail(LB_EINVAL, "%s: sizes M=%lld K=%lld V=%lld must lie in 0 <= M < 2^27, 1 <= K, V < 2^22", name,
+                    (long long)M, (long long)K, (long long)V);
+    return LB_OK;
+}
+
+// a caller's workspace
+int ws_check(const char *name, const void *ws, int64_t have, int64_t need) {
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 15) || have < need)
+        return fail(LB_EINVAL, "%s: the workspace must be 16-byte aligned and hold %lld bytes (%p, %lld given)", name,
+                    (long long)need, ws, (long long)have);
+    return LB_OK;
+}
+
 } // namespace
 
 namespace lb {
@@ -394,6 +418,78 @@ int softmax_bwd(const void *P, const void *dY, void *dX, int64_t rows, int64_t c
     if (e != hipSuccess)
         return hip_fail("softmax_bwd", e);
     return LB_OK;
+}
+
+int64_t lin_xent_workspace(int64_t M, int64_t K, int64_t V) {
+    tl_error.clear();
+    if (!xent_sizes_ok(M, K, V))
+        return xent_check("lin_xent_workspace", M, K, V, LB_BF16);
+    return M == 0 ? 0 : lb::xent::forward_bytes(M, K, V);
+}
+
+int64_t lin_xent_bwd_workspace(int64_t M, int64_t K, int64_t V) {
+    tl_error.clear();
+    if (!xent_sizes_ok(M, K, V))
+        return xent_check("lin_xent_bwd_workspace", M, K, V, LB_BF16);
+    return M == 0 ? 0 : lb::xent::backward_bytes(M, K, V);
+}
+
+int lin_xent(const void *X, const void *W, const int64_t *target, float *loss, float *lse, float *out, int64_t M,
+             int64_t K, int64_t V, int dtype, void *ws, int64_t ws_bytes) {
+    tl_error.clear();
+    if (int rc = xent_check("lin_xent", M, K, V, dtype))
+        return rc;
+    if (!out || (M > 0 && (!X || !W || !target || !loss || !lse)))
+        return fail(LB_EINVAL, "lin_xent: NULL buffer with M=%lld", (long long)M);
+    if (M > 0)
+        if (int rc = ws_check("lin_xent", ws, ws_bytes, lb::xent::forward_bytes(M, K, V)))
+            return rc;
+    lb::XentArgs a;
+    a.X = X;
+    a.W = W;
+    a.target = target;
+    a.loss = loss;
+    a.lse = lse;
+    a.out = out;
+    a.M = M;
+    a.K = K;
+    a.V = V;
+    a.f16 = dtype == LB_F16;
+    a.ws = ws;
+    hipError_t e = lb::launch_lin_xent(a, tl_stream);
+    return e == hipSuccess ? LB_OK : hip_fail("lin_xent", e);
+}
+
+int lin_xent_bwd(const void *X, const void *W, const int64_t *target, const float *lse, const float *row_scale,
+                 const float *d_scale, float scale, void *dX, void *dW, int64_t M, int64_t K, int64_t V, int dtype,
+                 void *ws, int64_t ws_bytes) {
+    tl_error.clear();
+    if (int rc = xent_check("lin_xent_bwd", M, K, V, dtype))
+        return rc;
+    if (!dX && !dW)
+        return LB_OK;
+    if (M > 0 && (!X || !W || !target || !lse))
+        return fail(LB_EINVAL, "lin_xent_bwd: NULL X, W, target or lse with M=%lld", (long long)M);
+    if (M > 0)
+        if (int rc = ws_check("lin_xent_bwd", ws, ws_bytes, lb::xent::backward_bytes(M, K, V)))
+            return rc;
+    lb::XentBwdArgs a;
+    a.X = X;
+    a.W = W;
+    a.target = target;
+    a.lse = lse;
+    a.row_scale = row_scale;
+    a.d_scale = d_scale;
+    a.scale = scale;
+    a.dX = dX;
+    a.dW = dW;
+    a.M = M;
+    a.K = K;
+    a.V = V;
+    a.f16 = dtype == LB_F16;
+    a.ws = ws;
+    hipError_t e = lb::launch_lin_xent_bwd(a, tl_stream);
+    return e == hipSuccess ? LB_OK : hip_fail("lin_xent_bwd", e);
 }
 
 int lb_set_stream(void *hip_stream) {

@@ -116,4 +116,33 @@ struct SoftmaxArgs {
 
 hipError_t launch_softmax_bwd(const SoftmaxArgs &a, hipStream_t s);
 
+// ---- softmax cross entropy of a Linear head ------------------------------
+struct XentArgs {
+    const void *X, *W;     // [M,K], [K,V], fp16 or bf16
+    const int64_t *target; // [M], negative: the row takes no part
+    float *loss, *lse;     // [M]
+    float *out;            // [0] mean loss, [1] 1 / counted rows
+    int64_t M, K, V;
+    bool f16;
+    void *ws; // xent::forward_bytes() of it
+};
+
+// 2-3 launches, and 2-3 more per further piece of the vocabulary
+hipError_t launch_lin_xent(const XentArgs &a, hipStream_t s);
+
+struct XentBwdArgs {
+    const void *X, *W;
+    const int64_t *target;
+    const float *lse;       // [M]
+    const float *row_scale; // [M] or null
+    const float *d_scale;   // device scalar or null
+    float scale;
+    void *dX, *dW; // [M,K], [K,V], the operands' type; null skips one
+    int64_t M, K, V;
+    bool f16;
+    void *ws; // xent::backward_bytes() of it
+};
+
+hipError_t launch_lin_xent_bwd(const XentBwdArgs &a, hipStream_t s);
+
 } // namespace lb

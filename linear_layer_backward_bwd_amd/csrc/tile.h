@@ -1,0 +1,465 @@
+// A 16-bit MFMA product tile for gfx950, shared by the loss-head and Muon kernels:
+//
+//     C[i,j] = Σ_r A(i,r)·B(j,r)        bf16 or fp16 operands, fp32 accumulation
+//
+// One block of four waves owns a TI x TJ tile of C and hands its fp32 sums to an
+// epilogue.  Each operand is stored in memory in one of two ways:
+//
+//   RC  reduction contiguous: A(i,r) = a[i*lda + r]
+//   OC  outer contiguous:     A(i,r) = a[r*lda + i]
+//
+// so that X·W, G·Wᵀ, Xᵀ·G, X·Xᵀ, Xᵀ·X and B·X all run without a transposed copy.
+//
+// Pipeline.  The reduction runs in pairs of 32-deep slabs (64 reduction indices).
+// An operand's pair is T x 64 elements in LDS, T*128 bytes, filled by global->LDS
+// DMA (buffer_load_dwordx4 ... lds) through a ring of S pair slots per operand:
+//
+//   RC  T rows of 128 B (whole cache lines); 16-byte chunk c of row o sits at
+//       chunk c ^ (o % 8); a 16x16x32 fragment is one ds_read_b128.
+//   OC  64 rows (r) of 2T bytes; chunk c of row r sits at
+//       c ^ 2*((r & 3) | 4*((r >> 3) & 1)); a fragment is two transposing reads
+//       (ds_read_b64_tr_b16), each a 4-row x 16-column block per 16 lanes.
+//
+// Both patterns read without bank conflicts (the layouts of the Linear backward's
+// tile kernel).  While the MFMAs of one slab run on fragments in registers, the
+// next slab's fragments are read; in a pair's second slab every fragment of the
+// pair is in registers, so after one barrier its slot takes the DMA of the pair S
+// ahead.  One barrier per 64 reduction indices.  Pairs past the reduction's end are
+// issued too, through an empty buffer descriptor (they read zero), so the loop has
+// no tail: only one wait count and one branch.
+//
+// Bound: MFMA for the 256x256 tile (8x8 fragments per wave: 16-24 KiB of LDS reads
+// per 64 MFMAs); the smaller tiles serve short sides, where HBM bounds the call.
+#pragma once
+
+#include "device.h"
+
+#include <type_traits>
+
+namespace lb {
+namespace tile {
+
+#define LB_LDS __attribute__((address_space(3)))
+
+constexpr uint32_t kOutOfRange = 0x80000000u; // buffer offset past every descriptor used here
+constexpr int kThreads = 256;                 // four waves
+
+// Two stored 16-bit types, told apart at compile time.
+struct BF16 {
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) { return pack_bf16x2(a, b); }
+    static __device__ __forceinline__ uint16_t one(float a) { return f32_to_bf16_bits(a); }
+    static __device__ __forceinline__ float f32(uint32_t h) { return bf16_bits_to_f32(h & 0xffffu); }
+    static __device__ __forceinline__ void mfma(f32x4_t &acc, const u32x4_t &a, const u32x4_t &b) {
+        asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    }
+};
+struct F16 {
+    static __device__ __forceinline__ uint16_t one(float a) {
+        return __builtin_bit_cast(uint16_t, (_Float16)a); // nearest even; overflow to infinity
+    }
+    static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+        return (uint32_t)one(a) | ((uint32_t)one(b) << 16);
+    }
+    static __device__ __forceinline__ float f32(uint32_t h) { return f16_bits_to_f32((uint16_t)(h & 0xffffu)); }
+    static __device__ __forceinline__ void mfma(f32x4_t &acc, const u32x4_t &a, const u32x4_t &b) {
+        asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+    }
+};
+
+// Four waves as WI x WJ, each FI x FJ fragments of 16 x 16; S pair slots.
+template <class T_, int WI_, int WJ_, int FI_, int FJ_, bool AOC_, bool BOC_, int S_>
+struct Cfg {
+    using T = T_;
+    static constexpr int WI = WI_, WJ = WJ_, FI = FI_, FJ = FJ_, S = S_;
+    static constexpr bool AOC = AOC_, BOC = BOC_;
+    static constexpr int TI = WI * FI * 16, TJ = WJ * FJ * 16;
+    static constexpr int kPairA = TI * 128, kPairB = TJ * 128; // bytes of an operand's pair
+    static constexpr int kOffB = S * kPairA;                   // A's slots first, then B's
+    static constexpr int kLds = S * (kPairA + kPairB);
+    static constexpr int kDmaA = TI / 32, kDmaB = TJ / 32; // DMA instructions per wave per pair
+    static constexpr int kDma = kDmaA + kDmaB;
+    static_assert(WI * WJ == 4, "four waves");
+    static_assert(TI % 32 == 0 && TJ % 32 == 0, "whole DMA instructions per wave");
+    static_assert(!AOC || TI == 128 || TI == 256, "OC rows of 256 or 512 bytes");
+    static_assert(!BOC || TJ == 128 || TJ == 256, "OC rows of 256 or 512 bytes");
+    static_assert(4 * FJ * 1024 <= kLds, "the epilogue stages 16 rows per wave in the ring");
+    static_assert((S - 2) * kDma < 64, "vmcnt is 6 bits");
+};
+
+// One product.  lda, ldb multiples of 8 elements, a and b 16-byte aligned.  Operands are
+// fetched in 16-byte chunks along their contiguous index: where that extent (RC: R, OC: I
+// or J) is no multiple of 8, the rest of the last chunk is memory of the operand's own,
+// and zero (or only reaches sums that the epilogue drops).  2*256*ld < 2^31 for RC
+// operands and 2*64*ld < 2^31 for OC ones, checked on the host.
+struct Job {
+    const uint16_t *a, *b;
+    int64_t lda, ldb;
+    int64_t I, J, R;
+    int tiles_i, tiles_j;
+    int group; // tile rows per raster group
+};
+
+typedef uint32_t frag_half_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, LB_LDS char *dst, uint32_t off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (LB_LDS void *)dst, 16, (int)off, 0, 0, 0);
+}
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// Publishes landed DMA and retires this wave's LDS reads; no fence, so DMA stays in flight.
+__device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+__device__ __forceinline__ int swz_oc(int row) { return 2 * ((row & 3) | (((row >> 3) & 1) << 2)); }
+
+// Block index -> tile.  Blocks are dealt to the 8 XCDs in turn, so each XCD's blocks are
+// first gathered into one contiguous range (any count), then rastered in groups of
+// `group` tile rows, so that tiles that run together share operand panels in that XCD's L2.
+__device__ __forceinline__ void coords(const Job &jb, int t, int &ti, int &tj) {
+    const int n = jb.tiles_i * jb.tiles_j;
+    const int x = t & 7, rem = n & 7;
+    int u = x * (n >> 3) + (x < rem ? x : rem) + (t >> 3);
+    const int per = jb.group * jb.tiles_j;
+    const int g = u / per;
+    const int first = g * jb.group;
+    const int rows = min(jb.tiles_i - first, jb.group);
+    u -= g * per;
+    ti = first + u % rows;
+    tj = u / rows;
+}
+
+// One operand of a tile: T outer indices from o0 on.
+template <int T, bool OC, int kDmaN, int S>
+struct Side {
+    static constexpr int kPair = T * 128;
+    static constexpr int kRowB = 2 * T; // OC row bytes
+    uint32_t off[kDmaN];                // DMA source offsets, fixed for the tile
+    const uint16_t *cur;                // first element of the next pair to fetch
+    int64_t step;                       // elements from one pair to the next
+    int64_t left;                       // reduction indices from `cur` on (may be <= 0)
+    int64_t ld, span;                   // RC: rows; OC: columns of the window
+    int kchunk;                         // RC: this lane's first r within a pair
+
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t ld_, int64_t O, int64_t R, int64_t o0, int w,
+                                         int lane) {
+        ld = ld_;
+        if constexpr (OC) {
+            left = R;
+            constexpr int kChunks = T / 8;       // 16-byte chunks per row
+            constexpr int kRows = 64 / kChunks;  // rows per DMA instruction
+            cur = p + o0;
+            step = 64 * ld;
+            span = (O - o0 + 7) / 8 * 8; // whole chunks
+            kchunk = 0;
+#pragma unroll
+            for (int d = 0; d < kDmaN; ++d) {
+                const int row = (w * kDmaN + d) * kRows + lane / kChunks;
+                const int c = (lane % kChunks) ^ swz_oc(row);
+                off[d] = (uint32_t)((row * ld + 8 * c) * 2) | ((uint32_t)!(8 * c < span) << 31);
+            }
+        } else {
+            left = (R + 7) / 8 * 8; // whole chunks
+            cur = p + o0 * ld;
+            step = 64;
+            span = min<int64_t>(T, O - o0);
+            kchunk = 8 * ((lane & 7) ^ (lane >> 3)); // row % 8 is lane / 8 in every instruction
+#pragma unroll
+            for (int d = 0; d < kDmaN; ++d) {
+                const int row = (w * kDmaN + d) * 8 + (lane >> 3);
+                off[d] = (uint32_t)((row * ld + kchunk) * 2) | ((uint32_t)!(row < span) << 31);
+            }
+        }
+    }
+    struct Src {
+        __amdgpu_buffer_rsrc_t rs;
+        uint32_t mask; // RC: bit 31 for lanes past the reduction's end
+    };
+    // the descriptor of the next pair; advances
+    __device__ __forceinline__ Src next() {
+        Src s;
+        if constexpr (OC) {
+            const int64_t rows = min<int64_t>(64, left);
+            s.rs = rsrc(cur, left > 0 ? (uint32_t)(((rows - 1) * ld + span) * 2) : 0u);
+            s.mask = 0;
+        } else {
+            s.rs = rsrc(cur, left > 0 ? (uint32_t)(((span - 1) * ld + left) * 2) : 0u);
+            s.mask = (uint32_t)(kchunk >= left) << 31;
+        }
+        cur += step;
+        left -= 64;
+        return s;
+    }
+    __device__ __forceinline__ void dma(const Src &s, LB_LDS char *slot, int w, int d) const {
+        dma16(s.rs, slot + (w * kDmaN + d) * 1024, off[d] | s.mask);
+    }
+};
+
+// LDS fragment addresses of one operand for a wave, and the reads.  Inline asm: the
+// compiler would wait for the DMA in flight (it may alias) before every read.  Callers
+// wait with settle(), which also keeps every output in use until the data has landed.
+template <int T, bool OC, int F, int S>
+struct Frags {
+    static constexpr int kPair = T * 128;
+    static constexpr int kReads = OC ? 2 * F : F;
+    LB_LDS char *base[OC ? F : 2];
+
+    __device__ __forceinline__ void init(LB_LDS char *region, int ob, int lane) {
+        if constexpr (OC) {
+            const int g = lane >> 4, s = lane & 15;
+            const int row = 8 * g + (s >> 2);
+#pragma unroll
+            for (int x = 0; x < F; ++x) {
+                const int col = ob + 16 * x + 4 * (s & 3);
+                base[x] = region + row * (2 * T) + (((col >> 3) ^ swz_oc(row)) << 4) + (col & 7) * 2;
+            }
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                base[h] = region + (ob + (lane & 15)) * 128 + (((4 * h + (lane >> 4)) ^ (lane & 7)) << 4);
+        }
+    }
+    // read number k (0..kReads-1) of slab half H; the slot is a compile-time constant
+    // where its offset fits the instruction's 16 bits (S == 2), else SLOT is 0 and `add` holds it
+    template <int SLOT, int H>
+    __device__ __forceinline__ void read(int k, int add, u32x4_t (&f)[F], frag_half_t (&h)[F][2]) const {
+        if constexpr (OC) {
+            const int x = k >> 1;
+            if (k & 1)
+                read_tr<SLOT * kPair + H * 64 * T + 8 * T>(base[x] + add, h[x][1]);
+            else
+                read_tr<SLOT * kPair + H * 64 * T>(base[x] + add, h[x][0]);
+        } else {
+            read_rc<SLOT * kPair, F>(base[H] + add, k, f);
+        }
+    }
+    template <int OFF>
+    static __device__ __forceinline__ void read_tr(const LB_LDS char *p, frag_half_t &v) {
+        static_assert(OFF >= 0 && OFF < 65536, "ds offset is 16 bits");
+        asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(v) : "v"(p), "n"(OFF));
+    }
+    template <int OFF, int N>
+    static __device__ __forceinline__ void read_rc(const LB_LDS char *p, int x, u32x4_t (&f)[N]) {
+        static_assert(OFF + 2048 * (N - 1) < 65536, "ds offset is 16 bits");
+        switch (x) { // x is a constant after unrolling
+        case 0: asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(f[0]) : "v"(p), "n"(OFF)); break;
+#define LB_RC(X)                                                                                                     \
+    case X:                                                                                                          \
+        if constexpr (X < N)                                                                                         \
+            asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(f[X < N ? X : 0]) : "v"(p), "n"(OFF + 2048 * X));    \
+        break;
+            LB_RC(1) LB_RC(2) LB_RC(3) LB_RC(4) LB_RC(5) LB_RC(6) LB_RC(7)
+#undef LB_RC
+        }
+    }
+    // after the wait: the reads' outputs exist from here on
+    static __device__ __forceinline__ void settle(u32x4_t (&f)[F], frag_half_t (&h)[F][2]) {
+        if constexpr (OC) {
+#pragma unroll
+            for (int x = 0; x < F; ++x) {
+                asm volatile("" : "+v"(h[x][0]), "+v"(h[x][1]));
+                f[x] = __builtin_shufflevector(h[x][0], h[x][1], 0, 1, 2, 3);
+            }
+        } else {
+#pragma unroll
+            for (int x = 0; x < F; ++x)
+                asm volatile("" : "+v"(f[x]));
+        }
+    }
+};
+
+// Wait states between the last MFMA and another instruction that reads its accumulator.
+__device__ __forceinline__ void mfma_drain() { asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" ::: "memory"); }
+
+template <class C>
+using Acc = f32x4_t[C::FI][C::FJ];
+
+// Keeps a row of accumulators in its AGPRs up to this point (the compiler otherwise
+// copies all of them to VGPRs before an epilogue's first branch, and spills).
+template <int N>
+__device__ __forceinline__ void pin(f32x4_t (&a)[N]) {
+#pragma unroll
+    for (int y = 0; y < N; ++y)
+        asm volatile("" : "+a"(a[y]));
+}
+
+// The sums of tile (ti, tj): acc[x][y] of lane l of wave w holds C[i][j..j+3] for
+// i = i0 + (w / WJ)*FI*16 + 16x + l % 16, j = j0 + (w % WJ)*FJ*16 + 16y + 4*(l / 16).
+// On return the ring is free (a barrier has passed) and may stage the epilogue.
+template <class C>
+__device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS char *smem, Acc<C> &acc) {
+    using SA = Side<C::TI, C::AOC, C::kDmaA, C::S>;
+    using SB = Side<C::TJ, C::BOC, C::kDmaB, C::S>;
+    using FA = Frags<C::TI, C::AOC, C::FI, C::S>;
+    using FB = Frags<C::TJ, C::BOC, C::FJ, C::S>;
+    constexpr int FI = C::FI, FJ = C::FJ, NM = FI * FJ;
+    constexpr int NR = FA::kReads + FB::kReads;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+    SA sa;
+    SB sb;
+    sa.init(jb.a, jb.lda, jb.I, jb.R, (int64_t)ti * C::TI, w, lane);
+    sb.init(jb.b, jb.ldb, jb.J, jb.R, (int64_t)tj * C::TJ, w, lane);
+    FA fa;
+    FB fb;
+    fa.init(smem, (w / C::WJ) * FI * 16, lane);
+    fb.init(smem + C::kOffB, (w % C::WJ) * FJ * 16, lane);
+#pragma unroll
+    for (int x = 0; x < FI; ++x)
+#pragma unroll
+        for (int y = 0; y < FJ; ++y)
+            acc[x][y] = f32x4_t{};
+
+    const int npair = (int)((jb.R + 63) / 64);
+    u32x4_t a0[FI], b0[FJ], a1[FI], b1[FJ];
+    frag_half_t ha[FI][2], hb[FJ][2];
+
+    auto issue = [&](const typename SA::Src &xa, const typename SB::Src &xb, int slot, int d) {
+        // the operands in turn where they have as many instructions
+        int op, k;
+        if constexpr (C::kDmaA == C::kDmaB) {
+            op = d & 1;
+            k = d >> 1;
+        } else {
+            op = d >= C::kDmaA;
+            k = op ? d - C::kDmaA : d;
+        }
+        if (op == 0)
+            sa.dma(xa, smem + slot * C::kPairA, w, k);
+        else
+            sb.dma(xb, smem + C::kOffB + slot * C::kPairB, w, k);
+    };
+    auto settle = [&](u32x4_t (&af)[FI], u32x4_t (&bf)[FJ]) {
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        FA::settle(af, ha);
+        FB::settle(bf, hb);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // MFMAs of one slab on (af, bf), the LDS reads of slab half H of the pair in slot
+    // SLOT (+ adds) into (an, bn) after the first of them, `other(i)` after each
+    auto slab = [&](auto slot_c, auto half_c, int add_a, int add_b, u32x4_t (&af)[FI], u32x4_t (&bf)[FJ],
+                    u32x4_t (&an)[FI], u32x4_t (&bn)[FJ], auto other) {
+        constexpr int SLOT = decltype(slot_c)::value, H = decltype(half_c)::value;
+        constexpr int kPer = (NR + NM - 1) / NM;                             // reads per MFMA
+        constexpr int kEvery = NR <= NM ? (NM / 2 / NR > 0 ? NM / 2 / NR : 1) : 1; // MFMAs per read
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+            C::T::mfma(acc[i / FJ][i % FJ], bf[i % FJ], af[i / FJ]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (i % kEvery == 0) {
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) {
+                    const int k = i / kEvery * kPer + e;
+                    if (k < FA::kReads)
+                        fa.template read<SLOT, H>(k, add_a, an, ha);
+                    else if (k < NR)
+                        fb.template read<SLOT, H>(k - FA::kReads, add_b, bn, hb);
+                }
+            }
+            other(i);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        settle(an, bn);
+    };
+    using Z = std::integral_constant<int, 0>;
+    using O = std::integral_constant<int, 1>;
+
+    // prologue: S pairs on their way; the first slab's fragments
+#pragma unroll
+    for (int s = 0; s < C::S; ++s) {
+        const auto xa = sa.next();
+        const auto xb = sb.next();
+#pragma unroll
+        for (int d = 0; d < C::kDma; ++d)
+            issue(xa, xb, s, d);
+    }
+    vm_wait<(C::S - 1) * C::kDma < 64 ? (C::S - 1) * C::kDma : 63>();
+    ring_barrier();
+#pragma unroll
+    for (int k = 0; k < FA::kReads; ++k)
+        fa.template read<0, 0>(k, 0, a0, ha);
+#pragma unroll
+    for (int k = 0; k < FB::kReads; ++k)
+        fb.template read<0, 0>(k, 0, b0, hb);
+    settle(a0, b0);
+
+    // one pair in slot SLOT (S == 2) or `slot`; NEXT: the following pair's slot
+    auto pair = [&](auto slot_c, auto next_c, int slot, int next) {
+        constexpr int SLOT = decltype(slot_c)::value;
+        constexpr bool fixed = C::S == 2;
+        const int aa = fixed ? 0 : slot * C::kPairA, ab = fixed ? 0 : slot * C::kPairB;
+        const int na = fixed ? 0 : next * C::kPairA, nb = fixed ? 0 : next * C::kPairB;
+        typename SA::Src xa;
+        typename SB::Src xb;
+        // first half; the descriptors of the pair S ahead are made between its MFMAs
+        slab(slot_c, O{}, aa, ab, a0, b0, a1, b1, [&](int i) {
+            if (i == NM - 2) {
+                xa = sa.next();
+                xb = sb.next();
+            }
+        });
+        vm_wait<(C::S - 2) * C::kDma>(); // the next pair has landed
+        ring_barrier();                  // everyone's; and this pair's slot is free
+        slab(next_c, Z{}, na, nb, a1, b1, a0, b0, [&](int i) {
+#pragma unroll
+            for (int d = i * C::kDma / NM; d < (i + 1) * C::kDma / NM; ++d)
+                issue(xa, xb, fixed ? SLOT : slot, d);
+        });
+    };
+    if constexpr (C::S == 2) {
+        // an odd count runs one pair of zeros more: with an exit between the two the
+        // compiler copied the accumulators out of the AGPRs on every turn
+        for (int q = 0; q < npair; q += 2) {
+            pair(Z{}, O{}, 0, 1);
+            pair(O{}, Z{}, 1, 0);
+        }
+    } else {
+        int slot = 0;
+        for (int q = 0; q < npair; ++q) {
+            const int next = slot + 1 == C::S ? 0 : slot + 1;
+            pair(Z{}, Z{}, slot, next);
+            slot = next;
+        }
+    }
+    mfma_drain();
+    vm_wait<0>();
+    ring_barrier();
+}
+
+// Passes a wave's sums through its own part of the ring, 16 rows at a time, so that a
+// lane holds 4 consecutive columns and 4*FJ lanes a row's FJ*16 columns (direct from the
+// accumulators a store instruction would touch 16 rows).  round(i, rows, j, v): v[q] is
+// C[i + q*rows][j..j+3], q < FJ.
+template <class C, class Fn>
+__device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_LDS char *smem, Fn round) {
+    constexpr int FJ = C::FJ, kChunks = 4 * FJ, kRows = 64 / kChunks;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    LB_LDS char *const reg = smem + w * (FJ * 1024);
+    const int64_t ib = i0 + (w / C::WJ) * C::FI * 16, jb = j0 + (w % C::WJ) * FJ * 16;
+#pragma unroll
+    for (int x = 0; x < C::FI; ++x) {
+        pin(acc[x]);
+#pragma unroll
+        for (int y = 0; y < FJ; ++y) {
+            const int r = lane & 15, c = 4 * y + (lane >> 4);
+            *reinterpret_cast<LB_LDS f32x4_t *>(reg + r * (FJ * 64) + ((c ^ (r & (kChunks - 1))) << 4)) = acc[x][y];
+        }
+        f32x4_t v[FJ];
+#pragma unroll
+        for (int q = 0; q < FJ; ++q) {
+            const int r = q * kRows + lane / kChunks, c = lane % kChunks;
+            v[q] = *reinterpret_cast<const LB_LDS f32x4_t *>(reg + r * (FJ * 64) + ((c ^ (r & (kChunks - 1))) << 4));
+        }
+        __builtin_amdgcn_sched_barrier(0); // all reads before the first use
+        round(ib + 16 * x + lane / kChunks, kRows, jb + 4 * (lane % kChunks), v);
+    }
+}
+
+} // namespace tile
+} // namespace lb
