@@ -325,6 +325,69 @@ int lin_xent_bwd(const void *X, const void *W, const int64_t *target, const floa
                  int64_t M, int64_t K, int64_t V, int dtype, void *ws, int64_t ws_bytes);
 
 /*
+ * muon_orth -- orthogonalises each matrix of a batch by Newton-Schulz products,
+ * as the Muon optimiser does with its momentum:
+ *     X = G / ‖G‖_F
+ *     steps times:  A = X·Xᵀ   B = b·A + c·A²   X = a·X + B·X
+ *     O = X                     (a, b, c) = (3.4445, −4.7750, 2.0315)
+ * which takes the singular values of G towards 1 and keeps its singular vectors
+ * (five steps bring singular values above about 1e-3 of ‖G‖_F to 0.7 ... 1.2).
+ * K > N runs the same polynomial on the columns (A = Xᵀ·X, X = a·X + X·B).
+ *
+ *   G   [batch,K,N]  g_dtype: LB_F32, LB_F16 or LB_BF16      read only
+ *   O   [batch,K,N]  o_dtype: LB_F16 or LB_BF16              written
+ *   steps  >= 1
+ *   ws  device memory of at least muon_workspace(batch, K, N) bytes, 16-byte
+ *       aligned, the caller's, as for lin_xent
+ *
+ * The products run on fp16 operands (fixed power-of-two scales keep them in range)
+ * with fp32 sums; the norm is summed in fp64.  X, A and B are rounded to 11 bits
+ * each: O is off by about 0.13% (relative Frobenius error) for spectra such as
+ * noise plus a few directions of the same energy.  Directions whose singular
+ * value is below about 2^-12 of the entries' scale are lost in that rounding, as
+ * they are in a 16-bit G.  A matrix of zeros gives zeros; one with an infinity or
+ * a NaN gives NaN throughout; the other matrices of the batch are not touched by
+ * it.  Results repeat bit for bit.  An empty batch or matrix is a no-op.
+ * Any alignment of the elements; 0 <= K, N < 2^20, 0 <= batch <= 65535.
+ * Errors: LB_EDTYPE for another dtype; LB_EINVAL for a size out of range,
+ * steps < 1, a NULL buffer or a workspace that is NULL, unaligned or too small;
+ * LB_EHIP when a launch fails.
+ */
+int64_t muon_workspace(int64_t batch, int64_t K, int64_t N);
+int muon_orth(const void *G, int g_dtype, void *O, int o_dtype, int64_t batch, int64_t K, int64_t N,
+              int steps, void *ws, int64_t ws_bytes);
+
+/*
+ * muon_step -- one Muon update of a batch of weight matrices (the Linear layers'
+ * W [K,N]; vectors and embeddings stay with AdamW), beside adamw_step_ex and with
+ * its optional parts:
+ *     g   = (float(grad) * inv_scale) * clip        clip = *d_clip, or 1 if NULL
+ *     mom = beta * mom + g
+ *     u   = nesterov ? g + beta * mom : mom
+ *     W   = W − lr·( scale · muon_orth(u) + wd·W )        (W on the right: before)
+ *     W16 = W rounded to nearest even, as w16_dtype       (if W16 is not NULL)
+ * and nothing at all is written to W, mom or W16 when d_skip is not NULL and
+ * *d_skip != 0.
+ *
+ *   W, mom     [batch,K,N] fp32, read and written in place
+ *   grad       [batch,K,N] grad_dtype: LB_F32, LB_F16 or LB_BF16, read only
+ *   scale      factor of the orthogonalised update; 0.2·sqrt(max(K, N)) gives it
+ *              the root mean square of an AdamW update, so lr can be AdamW's
+ *   beta       in [0, 1);  nesterov 0 or 1;  steps >= 1
+ *   d_clip, d_skip, W16, w16_dtype   as for adamw_step_ex
+ *   ws         as for muon_orth
+ *
+ * All arithmetic on W and mom is fp32; the orthogonalised update is not rounded
+ * to 16 bits (it stays in the last product's fp32 sums).  Errors: muon_orth's;
+ * LB_EINVAL for beta outside [0, 1); LB_EDTYPE for a W16 with a w16_dtype other
+ * than LB_BF16 / LB_F16.
+ */
+int muon_step(float *W, const void *grad, int grad_dtype, float *mom, int64_t batch, int64_t K, int64_t N,
+              float lr, float beta, float wd, float scale, int steps, int nesterov, float inv_scale,
+              const float *d_clip, const int32_t *d_skip, void *W16, int w16_dtype, void *ws,
+              int64_t ws_bytes);
+
+/*
  * lb_set_stream -- the HIP stream (a hipStream_t, passed as void*) on which
  * the calling thread's later calls enqueue their kernels; NULL selects the
  * null stream.  The setting is per thread.  Returns LB_OK.

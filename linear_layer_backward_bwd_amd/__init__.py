@@ -13,7 +13,7 @@ import os
 
 __all__ = ["lin_bwd", "lin_bwd_ex", "adamw_step", "adamw_step_f16", "adamw_step_bf16",
            "adamw_step_ex", "grad_norm", "softmax_bwd", "lin_xent", "lin_xent_bwd",
-           "lin_xent_workspace", "lin_xent_bwd_workspace", "lb_set_stream", "lb_set_lin_bwd_path",
+           "lin_xent_workspace", "lin_xent_bwd_workspace", "muon_orth", "muon_step", "muon_workspace", "lb_set_stream", "lb_set_lin_bwd_path",
            "lin_bwd_path", "lb_last_error", "lb_version", "lb_shutdown", "library", "LIB_PATH",
            "LB_F32", "LB_BF16", "LB_F16", "LB_PATH_AUTO", "LB_PATH_TILE", "LB_PATH_SMALL_M",
            "LB_PATH_GENERAL", "LB_PATH_FUSED_SMALL_M"]
@@ -60,6 +60,13 @@ def library() -> ctypes.CDLL:
     for name in ("lin_xent_workspace", "lin_xent_bwd_workspace"):
         getattr(lib, name).argtypes = [i64, i64, i64]
         getattr(lib, name).restype = i64
+    lib.muon_orth.argtypes = [vp, i32, vp, i32, i64, i64, i64, i32, vp, i64]
+    lib.muon_orth.restype = i32
+    lib.muon_step.argtypes = [vp, vp, i32, vp, i64, i64, i64, f32, f32, f32, f32, i32, i32, f32, vp, vp, vp,
+                              i32, vp, i64]
+    lib.muon_step.restype = i32
+    lib.muon_workspace.argtypes = [i64, i64, i64]
+    lib.muon_workspace.restype = i64
     lib.lb_set_stream.argtypes = [vp]
     lib.lb_set_stream.restype = i32
     lib.lb_set_lin_bwd_path.argtypes = [i32]
@@ -470,3 +477,85 @@ def lin_xent_workspace(M: int, K: int, V: int) -> int:
 def lin_xent_bwd_workspace(M: int, K: int, V: int) -> int:
     """Bytes of device memory that lin_xent_bwd needs for these sizes."""
     return _bytes("lin_xent_bwd_workspace", M, K, V)
+
+
+def muon_workspace(batch: int, K: int, N: int) -> int:
+    """Bytes of device memory that muon_orth and muon_step need for these sizes."""
+    return _bytes("muon_workspace", batch, K, N)
+
+
+def _matrices(t, name):
+    if t.dim() == 2:
+        return (1,) + tuple(t.shape)
+    if t.dim() == 3:
+        return tuple(t.shape)
+    raise ValueError("%s must be a matrix [K,N] or a batch of them [batch,K,N]" % name)
+
+
+def muon_orth(G, out=None, dtype=None, steps=5, ws=None):
+    """Newton-Schulz orthogonalisation of each matrix of G [K,N] or [batch,K,N] (C: muon_orth).
+
+    G: float32, float16 or bfloat16.  Returns out, of G's shape, bfloat16 (the default) or
+    float16 (dtype, or the type of a given out).  ws: device memory of at least
+    muon_workspace(batch, K, N) bytes, or None to take it from torch.
+    """
+    import torch
+    gd = {torch.float32: LB_F32, torch.float16: LB_F16, torch.bfloat16: LB_BF16}.get(G.dtype)
+    if gd is None:
+        raise TypeError("G must be float32, float16 or bfloat16")
+    batch, K, N = _matrices(G, "G")
+    if out is None:
+        out = torch.empty(G.shape, dtype=dtype or torch.bfloat16, device=G.device)
+    od = {torch.float16: LB_F16, torch.bfloat16: LB_BF16}.get(out.dtype)
+    if od is None or (dtype is not None and out.dtype != dtype):
+        raise TypeError("out must be bfloat16 or float16 (and of the dtype asked for)")
+    if out.shape != G.shape:
+        raise ValueError("out must have G's shape")
+    dev = _device_of([G, out, ws])
+    need = muon_workspace(batch, K, N)
+    with _on_device(dev):
+        ws = _workspace(ws, need, dev)
+        rc = library().muon_orth(_ptr(G), gd, _ptr(out), od, batch, K, N, int(steps), _ptr(ws),
+                                 ws.numel() * ws.element_size())
+        _check(rc, "muon_orth")
+    return out
+
+
+def muon_step(W, grad, mom, lr, beta, wd, scale=None, steps=5, nesterov=True, inv_scale=1.0, clip=None,
+              skip=None, w16=None, ws=None) -> None:
+    """One Muon update in place on W and mom (float32, [K,N] or [batch,K,N]; C: muon_step).
+
+    grad: float32, float16 or bfloat16, read only.  scale: factor of the orthogonalised
+    update, by default 0.2·sqrt(max(K, N)) (the size of an AdamW update).  clip, skip and
+    w16 as for adamw_step_ex; ws as for muon_orth.
+    """
+    import torch
+    gd = {torch.float32: LB_F32, torch.float16: LB_F16, torch.bfloat16: LB_BF16}.get(grad.dtype)
+    if gd is None:
+        raise TypeError("grad must be float32, float16 or bfloat16")
+    if W.dtype != torch.float32 or mom.dtype != torch.float32:
+        raise TypeError("W and mom must be float32")
+    batch, K, N = _matrices(W, "W")
+    if grad.shape != W.shape or mom.shape != W.shape:
+        raise ValueError("W, grad and mom must have one shape")
+    if clip is not None and (clip.dtype != torch.float32 or clip.numel() != 1):
+        raise TypeError("clip must be a one-element float32 tensor")
+    if skip is not None and (skip.dtype != torch.int32 or skip.numel() != 1):
+        raise TypeError("skip must be a one-element int32 tensor")
+    wd16 = 0
+    if w16 is not None:
+        wd16 = {torch.bfloat16: LB_BF16, torch.float16: LB_F16}.get(w16.dtype)
+        if wd16 is None:
+            raise TypeError("w16 must be bfloat16 or float16")
+        if w16.shape != W.shape:
+            raise ValueError("w16 must have W's shape")
+    if scale is None:
+        scale = 0.2 * max(K, N) ** 0.5
+    dev = _device_of([W, grad, mom, clip, skip, w16, ws])
+    need = muon_workspace(batch, K, N)
+    with _on_device(dev):
+        ws = _workspace(ws, need, dev)
+        rc = library().muon_step(_ptr(W), _ptr(grad), gd, _ptr(mom), batch, K, N, lr, beta, wd, scale, int(steps),
+                                 int(bool(nesterov)), inv_scale, _ptr(clip), _ptr(skip), _ptr(w16), wd16, _ptr(ws),
+                                 ws.numel() * ws.element_size())
+        _check(rc, "muon_step")

@@ -13,7 +13,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "liblinbwd.so")
 SOURCES = ["api.hip", "lin_bwd.hip", "adamw.hip", "grad_norm.hip", "bias_grad.hip", "softmax_bwd.hip",
-           "xent.hip"]
+           "xent.hip", "muon.hip"]
 # measurement only (bench.py): copy / read / AdamW-mix stream and MFMA peak kernels
 CALIB_PATH = os.path.join(HERE, "libcalib.so")
 CALIB_SOURCES = ["calib.hip"]

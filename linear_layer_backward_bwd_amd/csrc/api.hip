@@ -10,6 +10,7 @@
 
 #include "../../include/linbwd.h"
 #include "kernels.h"
+#include "plan_muon.h"
 #include "plan_xent.h"
 
 namespace {
@@ -267,6 +268,42 @@ int ws_check(const char *name, const void *ws, int64_t have, int64_t need) {
     return LB_OK;
 }
 
+bool grad_type(int dtype, lb::GradType &gt) {
+    switch (dtype) {
+    case LB_F32: gt = lb::GRAD_F32; return true;
+    case LB_F16: gt = lb::GRAD_F16; return true;
+    case LB_BF16: gt = lb::GRAD_BF16; return true;
+    default: return false;
+    }
+}
+
+int muon_sizes(const char *name, int64_t batch, int64_t K, int64_t N) {
+    if (batch < 0 || batch > lb::muon::kMaxBatch || K < 0 || N < 0 || K >= lb::muon::kMaxSide ||
+        N >= lb::muon::kMaxSide)
+        return fail(LB_EINVAL, "%s: sizes batch=%lld K=%lld N=%lld must lie in 0 <= batch <= 65535, 0 <= K, N < 2^20",
+                    name, (long long)batch, (long long)K, (long long)N);
+    return LB_OK;
+}
+
+// checks what muon_orth and muon_step share, then launches
+int muon_impl(const char *name, lb::MuonArgs &a, int g_dtype, int steps, int64_t ws_bytes) {
+    if (!grad_type(g_dtype, a.gt))
+        return fail(LB_EDTYPE, "%s: dtype %d is not LB_F32, LB_F16 or LB_BF16", name, g_dtype);
+    if (int rc = muon_sizes(name, a.batch, a.K, a.N))
+        return rc;
+    if (steps < 1)
+        return fail(LB_EINVAL, "%s: steps = %d must be at least 1", name, steps);
+    if (a.batch == 0 || a.K == 0 || a.N == 0)
+        return LB_OK;
+    if (!a.grad || (a.O ? false : !a.W || !a.mom))
+        return fail(LB_EINVAL, "%s: NULL buffer", name);
+    if (int rc = ws_check(name, a.ws, ws_bytes, lb::muon::plan(a.batch, a.K, a.N).bytes))
+        return rc;
+    a.steps = steps;
+    hipError_t e = lb::launch_muon(a, tl_stream);
+    return e == hipSuccess ? LB_OK : hip_fail(name, e);
+}
+
 } // namespace
 
 namespace lb {
@@ -490,6 +527,62 @@ int lin_xent_bwd(const void *X, const void *W, const int64_t *target, const floa
     a.ws = ws;
     hipError_t e = lb::launch_lin_xent_bwd(a, tl_stream);
     return e == hipSuccess ? LB_OK : hip_fail("lin_xent_bwd", e);
+}
+
+int64_t muon_workspace(int64_t batch, int64_t K, int64_t N) {
+    tl_error.clear();
+    if (int rc = muon_sizes("muon_workspace", batch, K, N))
+        return rc;
+    return batch == 0 || K == 0 || N == 0 ? 0 : lb::muon::plan(batch, K, N).bytes;
+}
+
+int muon_orth(const void *G, int g_dtype, void *O, int o_dtype, int64_t batch, int64_t K, int64_t N, int steps,
+              void *ws, int64_t ws_bytes) {
+    tl_error.clear();
+    if (o_dtype != LB_BF16 && o_dtype != LB_F16)
+        return fail(LB_EDTYPE, "muon_orth: o_dtype %d is not LB_BF16 or LB_F16", o_dtype);
+    if (!O && batch > 0 && K > 0 && N > 0)
+        return fail(LB_EINVAL, "muon_orth: NULL O");
+    lb::MuonArgs a;
+    a.grad = G;
+    a.batch = batch;
+    a.K = K;
+    a.N = N;
+    a.ws = ws;
+    a.O = O;
+    a.o_bf16 = o_dtype == LB_BF16;
+    return muon_impl("muon_orth", a, g_dtype, steps, ws_bytes);
+}
+
+int muon_step(float *W, const void *grad, int grad_dtype, float *mom, int64_t batch, int64_t K, int64_t N, float lr,
+              float beta, float wd, float scale, int steps, int nesterov, float inv_scale, const float *d_clip,
+              const int32_t *d_skip, void *W16, int w16_dtype, void *ws, int64_t ws_bytes) {
+    tl_error.clear();
+    if (!beta_ok(beta))
+        return fail(LB_EINVAL, "muon_step: beta = %g must lie in [0, 1)", (double)beta);
+    if (W16 && w16_dtype != LB_BF16 && w16_dtype != LB_F16)
+        return fail(LB_EDTYPE, "muon_step: w16_dtype %d is not LB_BF16 or LB_F16", w16_dtype);
+    if (W16 && (W16 == (void *)W || W16 == grad || W16 == (void *)mom))
+        return fail(LB_EINVAL, "muon_step: the 16-bit copy must not alias W, grad or mom");
+    lb::MuonArgs a;
+    a.grad = grad;
+    a.batch = batch;
+    a.K = K;
+    a.N = N;
+    a.ws = ws;
+    a.W = W;
+    a.mom = mom;
+    a.W16 = W16;
+    a.o_bf16 = w16_dtype == LB_BF16;
+    a.lr = lr;
+    a.beta = beta;
+    a.wd = wd;
+    a.scale = scale;
+    a.inv_scale = inv_scale;
+    a.nesterov = nesterov != 0;
+    a.clip = d_clip;
+    a.skip = d_skip;
+    return muon_impl("muon_step", a, grad_dtype, steps, ws_bytes);
 }
 
 int lb_set_stream(void *hip_stream) {

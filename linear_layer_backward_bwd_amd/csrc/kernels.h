@@ -145,4 +145,28 @@ struct XentBwdArgs {
 
 hipError_t launch_lin_xent_bwd(const XentBwdArgs &a, hipStream_t s);
 
+// ---- Muon -----------------------------------------------------------------
+struct MuonArgs {
+    const void *grad; // [batch][K][N]
+    GradType gt;
+    int64_t batch, K, N;
+    int steps;
+    void *ws; // muon::plan().bytes of it
+    // orthogonalisation only: O [batch][K][N], 16 bit; then W and mom are null
+    void *O = nullptr;
+    bool o_bf16 = true; // type of O or W16
+    // the update: momentum and weights in place
+    float *W = nullptr;
+    float *mom = nullptr;
+    void *W16 = nullptr; // or null
+    float lr = 0, beta = 0, wd = 0, scale = 0;
+    float inv_scale = 1;
+    bool nesterov = false;
+    const float *clip = nullptr;   // device scalar or null
+    const int32_t *skip = nullptr; // device flag: nonzero -> write nothing, or null
+};
+
+// 2 launches and 3 per step
+hipError_t launch_muon(const MuonArgs &a, hipStream_t s);
+
 } // namespace lb

@@ -1,0 +1,413 @@
+// Muon on gfx950: momentum, Newton-Schulz orthogonalisation, weight update.
+//
+//     g = float(grad)·inv_scale·clip      mom = β·mom + g
+//     u = g + β·mom (Nesterov) or mom     X = u / ‖u‖_F
+//     repeat: A = X·Xᵀ   B = b·A + c·A²   X = a·X + B·X       (a, b, c below)
+//     W = W − lr·(scale·X + wd·W)
+//
+// The polynomial a·σ + b·σ³ + c·σ⁵ acts on the singular values of X and moves all of
+// them towards 1.  The products run on the shorter side: A = X·Xᵀ for K <= N, XᵀX and
+// X·B for K > N; with the tile's two operand layouts no transpose is stored.
+//
+// Numbers.  All operands of the products are fp16 (11 bits; bf16's 8 gave errors of 1%
+// after five steps on noise, fp16 0.13%), scaled by fixed powers of two: singular
+// values stay in [0, 1.21] (the polynomial's maximum on that interval is 1.202), so
+// |X| <= 1.21, |A| <= 1.47 and |B| <= 2.81 entry by entry, and 2^15·X, 2^14·A, 2^14·B stay
+// below 65504 while entries down to 2^-29 of the largest singular value keep 11 bits.
+// Sums are fp32; the norm is summed in fp64; momentum and W are fp32 throughout.
+// Each X, A and B is rounded once.
+#include "kernels.h"
+#include "plan_muon.h"
+#include "tile.h"
+
+#include <algorithm>
+
+namespace lb {
+namespace {
+
+using namespace tile;
+using muon::cdiv;
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kX = 32768.0f; // 2^15: stored X / X
+constexpr float kG = 16384.0f; // 2^14: stored A / A, stored B / B
+
+// ---- momentum and norm -------------------------------------------------------------------
+template <int GT>
+__device__ __forceinline__ float grad_at(const void *g, int64_t i) {
+    if constexpr (GT == GRAD_F32)
+        return static_cast<const float *>(g)[i];
+    else if constexpr (GT == GRAD_F16)
+        return f16_bits_to_f32(static_cast<const uint16_t *>(g)[i]);
+    else
+        return bf16_bits_to_f32(static_cast<const uint16_t *>(g)[i]);
+}
+// four elements at i (i and the buffer aligned to them)
+template <int GT>
+__device__ __forceinline__ f32x4_t grad4_at(const void *g, int64_t i) {
+    if constexpr (GT == GRAD_F32) {
+        return *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(g) + i);
+    } else {
+        const u32x2_t h = *reinterpret_cast<const u32x2_t *>(static_cast<const uint16_t *>(g) + i);
+        if constexpr (GT == GRAD_F16)
+            return f32x4_t{F16::f32(h[0]), F16::f32(h[0] >> 16), F16::f32(h[1]), F16::f32(h[1] >> 16)};
+        else
+            return f32x4_t{BF16::f32(h[0]), BF16::f32(h[0] >> 16), BF16::f32(h[1]), BF16::f32(h[1] >> 16)};
+    }
+}
+
+struct PrepParams {
+    const void *g;
+    float *mom; // or null: u = g
+    int64_t K, N, Np;
+    float inv_scale, beta;
+    const float *clip;
+    const int32_t *skip;
+    int nesterov, parts;
+    double *part; // [batch][parts]
+    uint16_t *x;  // [batch][K][Np]
+};
+
+__device__ __forceinline__ float unscaled(float g, float inv_scale, float clip) {
+    return __fmul_rn(__fmul_rn(g, inv_scale), clip);
+}
+__device__ __forceinline__ float update_of(float g, float mom, const PrepParams &p) {
+    return !p.mom ? g : p.nesterov ? __fadd_rn(g, __fmul_rn(p.beta, mom)) : mom;
+}
+
+// mom is updated in place; block j of a matrix sums u² over its share (fixed order).
+// HBM-bound: one read of grad, one read and write of mom.
+template <int GT, bool VEC>
+__global__ __launch_bounds__(256) void k_muon_norm(PrepParams p) {
+    if (p.skip && *p.skip)
+        return;
+    __shared__ double sh[256];
+    const float clip = p.clip ? *p.clip : 1.0f;
+    const int64_t n = p.K * p.N, base = (int64_t)blockIdx.y * n;
+    double s = 0.0;
+    constexpr int kN = VEC ? 4 : 1;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * kN; i < n; i += (int64_t)p.parts * 256 * kN) {
+        f32x4_t g{}, m{};
+        if constexpr (VEC)
+            g = grad4_at<GT>(p.g, base + i);
+        else
+            g[0] = grad_at<GT>(p.g, base + i);
+        if (p.mom) {
+            if constexpr (VEC)
+                m = *reinterpret_cast<const f32x4_t *>(p.mom + base + i);
+            else
+                m[0] = p.mom[base + i];
+        }
+#pragma unroll
+        for (int e = 0; e < kN; ++e) {
+            g[e] = unscaled(g[e], p.inv_scale, clip);
+            m[e] = __fadd_rn(__fmul_rn(p.beta, m[e]), g[e]);
+            const double u = (double)update_of(g[e], m[e], p);
+            s += u * u;
+        }
+        if (p.mom) {
+            if constexpr (VEC)
+                *reinterpret_cast<f32x4_t *>(p.mom + base + i) = m;
+            else
+                p.mom[base + i] = m[0];
+        }
+    }
+    sh[threadIdx.x] = s;
+    __syncthreads();
+    for (int h = 128; h > 0; h >>= 1) {
+        if ((int)threadIdx.x < h)
+            sh[threadIdx.x] += sh[threadIdx.x + h];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0)
+        p.part[(int64_t)blockIdx.y * p.parts + blockIdx.x] = sh[0];
+}
+
+// X = u / ‖u‖_F in fp16, rows padded with zeros to a multiple of 8.  ‖u‖ = 0 gives 0, a
+// norm that is infinite or NaN gives NaN throughout.
+template <int GT, bool VEC>
+__global__ __launch_bounds__(256) void k_muon_scale(PrepParams p) {
+    if (p.skip && *p.skip)
+        return;
+    __shared__ double sh[256];
+    sh[threadIdx.x] = (int)threadIdx.x < p.parts ? p.part[(int64_t)blockIdx.y * p.parts + threadIdx.x] : 0.0;
+    __syncthreads();
+    for (int h = 128; h > 0; h >>= 1) {
+        if ((int)threadIdx.x < h)
+            sh[threadIdx.x] += sh[threadIdx.x + h];
+        __syncthreads();
+    }
+    const double norm = sqrt(sh[0]);
+    const double f = norm == 0.0 ? 0.0 : norm < INFINITY ? (double)kX / norm : NAN;
+    const float clip = p.clip ? *p.clip : 1.0f;
+    const int64_t base = (int64_t)blockIdx.y * p.K * p.N;
+    uint16_t *const x = p.x + (int64_t)blockIdx.y * p.K * p.Np;
+    const int64_t per = p.Np / 4, n = p.K * per;
+    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (int64_t)gridDim.x * 256) {
+        const int64_t r = q / per, c = (q - r * per) * 4, i = base + r * p.N + c;
+        f32x4_t g{}, m{};
+        if (VEC && c < p.N) {
+            g = grad4_at<GT>(p.g, i);
+            if (p.mom)
+                m = *reinterpret_cast<const f32x4_t *>(p.mom + i);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < p.N) {
+                    g[e] = grad_at<GT>(p.g, i + e);
+                    m[e] = p.mom ? p.mom[i + e] : 0.0f;
+                }
+        }
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float u = update_of(unscaled(g[e], p.inv_scale, clip), m[e], p);
+            h[e] = c + e < p.N ? F16::one((float)((double)u * f)) : (uint16_t)0;
+        }
+        *reinterpret_cast<u32x2_t *>(x + r * p.Np + c) =
+            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+    }
+}
+
+// ---- the products -------------------------------------------------------------------------
+enum Step {
+    GRAM,   // out = f·sum
+    ADD,    // out = f·sum + fa·add
+    ORTH,   // o = (f·sum + fa·add), 16 bit, the caller's matrix
+    UPDATE, // W -= lr·(scale·(f·sum + fa·add) + wd·W), and its 16-bit copy
+};
+
+struct ProductParams {
+    Job job;
+    int64_t step_a, step_b; // elements from one matrix to the next
+    float f, fa;
+    const uint16_t *add; // fp16
+    int64_t ld_add, step_add;
+    uint16_t *out; // fp16, ld a multiple of 8
+    int64_t ld_out, step_out;
+    // the caller's matrices, [batch][I][J]
+    uint16_t *o;
+    float *W;
+    uint16_t *W16;
+    int o_bf16; // type of o / W16
+    float lr, scale, wd;
+    const int32_t *skip;
+};
+
+// VEC: rows of the caller's matrices take 4 elements at a time.
+template <class C, int STEP, bool VEC>
+__global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_muon_product(ProductParams p) {
+    if (p.skip && *p.skip)
+        return;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
+    LB_LDS char *smem = (LB_LDS char *)smem_raw;
+    const int64_t b = blockIdx.y;
+    Job job = p.job;
+    job.a += b * p.step_a;
+    job.b += b * p.step_b;
+    int ti, tj;
+    coords(job, blockIdx.x, ti, tj);
+    Acc<C> acc;
+    accumulate<C>(job, ti, tj, smem, acc);
+    const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
+    const int64_t I = job.I, J = job.J, Jp = (J + 7) / 8 * 8;
+    const uint16_t *const add = p.add + b * p.step_add;
+    uint16_t *const out = p.out + b * p.step_out;
+    const int64_t mine = b * I * J;
+    staged<C>(acc, i0, j0, smem, [&](int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
+        u32x2_t x[C::FJ];
+        f32x4_t w[C::FJ];
+        if constexpr (STEP != GRAM) {
+#pragma unroll
+            for (int q = 0; q < C::FJ; ++q) {
+                const int64_t r = i + q * rows;
+                const bool in = r < I && j < Jp;
+                x[q] = in ? *reinterpret_cast<const u32x2_t *>(add + r * p.ld_add + j) : u32x2_t{};
+                if constexpr (STEP == UPDATE && VEC)
+                    w[q] = r < I && j < J ? *reinterpret_cast<const f32x4_t *>(p.W + mine + r * J + j) : f32x4_t{};
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < C::FJ; ++q) {
+            const int64_t r = i + q * rows;
+            f32x4_t t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                t[e] = p.f * v[q][e];
+            if constexpr (STEP != GRAM) {
+                const float a[4] = {F16::f32(x[q][0]), F16::f32(x[q][0] >> 16), F16::f32(x[q][1]),
+                                    F16::f32(x[q][1] >> 16)};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    t[e] = __builtin_fmaf(p.fa, a[e], t[e]);
+            }
+            if (r >= I)
+                continue;
+            if constexpr (STEP == GRAM || STEP == ADD) {
+                if (j < Jp)
+                    *reinterpret_cast<u32x2_t *>(out + r * p.ld_out + j) =
+                        u32x2_t{F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
+            } else if constexpr (STEP == ORTH) {
+                uint16_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = p.o_bf16 ? BF16::one(t[e]) : F16::one(t[e]);
+                uint16_t *const o = p.o + mine + r * J + j;
+                if constexpr (VEC) {
+                    if (j < J)
+                        *reinterpret_cast<u32x2_t *>(o) =
+                            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < J)
+                            o[e] = h[e];
+                }
+            } else {
+                const int64_t at = mine + r * J + j;
+                auto stepped = [&](float old, float o) { return old - p.lr * (p.scale * o + p.wd * old); };
+                if constexpr (VEC) {
+                    if (j >= J)
+                        continue;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[q][e] = stepped(w[q][e], t[e]);
+                    *reinterpret_cast<f32x4_t *>(p.W + at) = w[q];
+                    if (p.W16)
+                        *reinterpret_cast<u32x2_t *>(p.W16 + at) =
+                            p.o_bf16 ? u32x2_t{BF16::pack2(w[q][0], w[q][1]), BF16::pack2(w[q][2], w[q][3])}
+                                     : u32x2_t{F16::pack2(w[q][0], w[q][1]), F16::pack2(w[q][2], w[q][3])};
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j + e < J) {
+                            const float nw = stepped(p.W[at + e], t[e]);
+                            p.W[at + e] = nw;
+                            if (p.W16)
+                                p.W16[at + e] = p.o_bf16 ? BF16::one(nw) : F16::one(nw);
+                        }
+                }
+            }
+        }
+    });
+}
+
+template <class C, int STEP, bool VEC>
+void launch(ProductParams &p, int64_t batch, hipStream_t s) {
+    p.job.tiles_i = (int)cdiv(p.job.I, C::TI);
+    p.job.tiles_j = (int)cdiv(p.job.J, C::TJ);
+    p.job.group = 4;
+    hipLaunchKernelGGL((k_muon_product<C, STEP, VEC>), dim3((unsigned)(p.job.tiles_i * p.job.tiles_j), (unsigned)batch),
+                       dim3(kThreads), 0, s, p);
+}
+template <bool AOC, bool BOC, int STEP, bool VEC = true>
+void product(ProductParams &p, int64_t batch, hipStream_t s) {
+    if (muon::big_tiles(batch, p.job.I, p.job.J))
+        launch<Cfg<F16, 2, 2, 8, 8, AOC, BOC, 2>, STEP, VEC>(p, batch, s);
+    else
+        launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 2>, STEP, VEC>(p, batch, s);
+}
+// the last product, on the caller's matrices
+template <int STEP>
+void last_product(ProductParams &p, int64_t batch, bool tall, bool vec, hipStream_t s) {
+    if (tall)
+        vec ? product<false, false, STEP, true>(p, batch, s) : product<false, false, STEP, false>(p, batch, s);
+    else
+        vec ? product<false, true, STEP, true>(p, batch, s) : product<false, true, STEP, false>(p, batch, s);
+}
+
+template <int GT>
+void prepare(PrepParams &p, int64_t batch, bool vec, hipStream_t s) {
+    const dim3 norm((unsigned)p.parts, (unsigned)batch);
+    const dim3 scale((unsigned)std::min<int64_t>(cdiv(p.K * p.Np / 4, 256), 8 * muon::kCUs), (unsigned)batch);
+    if (vec) {
+        hipLaunchKernelGGL((k_muon_norm<GT, true>), norm, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((k_muon_scale<GT, true>), scale, dim3(256), 0, s, p);
+    } else {
+        hipLaunchKernelGGL((k_muon_norm<GT, false>), norm, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((k_muon_scale<GT, false>), scale, dim3(256), 0, s, p);
+    }
+}
+
+bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+} // namespace
+
+hipError_t launch_muon(const MuonArgs &a, hipStream_t s) {
+    if (a.batch == 0 || a.K == 0 || a.N == 0)
+        return hipSuccess;
+    const muon::Plan pl = muon::plan(a.batch, a.K, a.N);
+    char *const ws = static_cast<char *>(a.ws);
+    uint16_t *x = reinterpret_cast<uint16_t *>(ws + pl.off_x0), *y = reinterpret_cast<uint16_t *>(ws + pl.off_x1);
+    uint16_t *const ga = reinterpret_cast<uint16_t *>(ws + pl.off_a);
+    uint16_t *const gb = reinterpret_cast<uint16_t *>(ws + pl.off_b);
+    PrepParams pp{a.grad, a.mom, a.K, a.N, pl.Np, a.inv_scale, a.beta, a.clip, a.skip, a.nesterov ? 1 : 0, pl.parts,
+                  reinterpret_cast<double *>(ws + pl.off_part), x};
+    const bool vec = a.N % 4 == 0 && aligned(a.grad, a.gt == GRAD_F32 ? 16 : 8) && aligned(a.mom, 16);
+    if (a.gt == GRAD_F32)
+        prepare<GRAD_F32>(pp, a.batch, vec, s);
+    else if (a.gt == GRAD_F16)
+        prepare<GRAD_F16>(pp, a.batch, vec, s);
+    else
+        prepare<GRAD_BF16>(pp, a.batch, vec, s);
+
+    const int64_t nx = a.K * pl.Np, ng = pl.s * pl.sp;
+    ProductParams gram{}, poly{}, upd{};
+    gram.job = Job{nullptr, nullptr, pl.Np, pl.Np, pl.s, pl.s, pl.tall ? a.K : a.N, 0, 0, 0};
+    gram.step_a = gram.step_b = nx;
+    gram.f = kG / (kX * kX);
+    gram.out = ga;
+    gram.ld_out = pl.sp;
+    gram.step_out = ng;
+    gram.skip = a.skip;
+    poly.job = Job{ga, ga, pl.sp, pl.sp, pl.s, pl.s, pl.s, 0, 0, 0};
+    poly.step_a = poly.step_b = poly.step_add = poly.step_out = ng;
+    poly.f = kC / kG;
+    poly.fa = kB;
+    poly.add = ga;
+    poly.ld_add = poly.ld_out = pl.sp;
+    poly.out = gb;
+    poly.skip = a.skip;
+    upd.job = Job{nullptr, nullptr, 0, 0, a.K, a.N, pl.s, 0, 0, 0};
+    upd.job.lda = pl.tall ? pl.Np : pl.sp;
+    upd.job.ldb = pl.tall ? pl.sp : pl.Np;
+    upd.step_a = pl.tall ? nx : ng;
+    upd.step_b = pl.tall ? ng : nx;
+    upd.ld_add = upd.ld_out = pl.Np;
+    upd.step_add = upd.step_out = nx;
+    upd.o = static_cast<uint16_t *>(a.O);
+    upd.W = a.W;
+    upd.W16 = static_cast<uint16_t *>(a.W16);
+    upd.o_bf16 = a.o_bf16 ? 1 : 0;
+    const bool rows4 = a.N % 4 == 0 && aligned(a.O, 8) && aligned(a.W, 16) && aligned(a.W16, 8);
+    upd.lr = a.lr;
+    upd.scale = a.scale;
+    upd.wd = a.wd;
+    upd.skip = a.skip;
+    for (int t = 0; t < a.steps; ++t) {
+        gram.job.a = gram.job.b = x;
+        if (pl.tall)
+            product<true, true, GRAM>(gram, a.batch, s);
+        else
+            product<false, false, GRAM>(gram, a.batch, s);
+        product<false, false, ADD>(poly, a.batch, s);
+        const bool last = t + 1 == a.steps;
+        upd.job.a = pl.tall ? x : gb;
+        upd.job.b = pl.tall ? gb : x;
+        upd.add = x;
+        upd.out = y;
+        // stored X is 2^15·X, the sum 2^29·B·X; the last step leaves the powers of two
+        upd.f = last ? 1.0f / (kX * kG) : 1.0f / kG;
+        upd.fa = last ? kA / kX : kA;
+        if (!last)
+            pl.tall ? product<false, false, ADD>(upd, a.batch, s) : product<false, true, ADD>(upd, a.batch, s);
+        else if (a.W)
+            last_product<UPDATE>(upd, a.batch, pl.tall, rows4, s);
+        else
+            last_product<ORTH>(upd, a.batch, pl.tall, rows4, s);
+        std::swap(x, y);
+    }
+    return hipGetLastError();
+}
+
+} // namespace lb

@@ -1,0 +1,338 @@
+"""GPU parity of the Muon entry points (muon_orth, muon_step) with a plain float64 iteration.
+
+Bound of the orthogonalisation.  The kernels round X, A and B to fp16 once per step (scaled
+by powers of two, so 11 bits relative to each entry) and sum in fp32, 2^-13 of such a
+rounding.  What a rounding of X does to the result depends on the spectrum: noise of 2^-11
+of the entries' size is 2^-11 * ||X||_F / sigma of a direction with singular value sigma,
+and the iteration brings every sigma to about 1.  No fixed number bounds that, so each test
+measures it in float64 on its own inputs: the iteration with roundings to 11 bits at the
+same places, in four realisations (rounding c*x for c = 1, 1.19, 1.41, 1.68, which moves
+every rounding point but not the errors' size).  The kernel's error is one more realisation
+of the same sum of some 15 independent uniform errors per entry (c = 1, but where an fp32
+sum tips a rounding): its norm is held to twice the largest of the four, each entry to 8
+times that in the root mean square.  16-bit outputs add half a step of their type.
+"""
+import math
+
+import pytest
+import torch
+
+import linear_layer_backward_bwd_amd as lb
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+H = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+NS = (3.4445, -4.7750, 2.0315)
+
+
+def place(t, offset=0):
+    buf = torch.full((t.numel() + 128 + offset,), -77.0, dtype=t.dtype, device=DEV)
+    v = buf[64 + offset:64 + offset + t.numel()].view(t.shape)
+    v.copy_(t)
+    v.whole = buf
+    return v
+
+
+def check_guards(v):
+    n, lo = v.numel(), (v.data_ptr() - v.whole.data_ptr()) // v.element_size()
+    assert bool((v.whole[:lo] == -77.0).all()) and bool((v.whole[lo + n:] == -77.0).all())
+
+
+def gradient(shape, seed, std=1e-4):
+    """Noise, and four directions of together the same energy."""
+    g = torch.Generator().manual_seed(seed)
+    B, K, N = shape
+    r = min(4, K, N)
+    strong = torch.randn(B, K, r, generator=g) @ torch.randn(B, r, N, generator=g) / r ** 0.5
+    return (torch.randn(shape, generator=g) + strong) * std
+
+
+def iterate(G, steps, rnd):
+    a, b, c = NS
+    X = G.double()
+    n = torch.linalg.matrix_norm(X, keepdim=True)
+    X = torch.where(n > 0, X / n, 0.0)
+    wide = X.shape[-2] <= X.shape[-1]
+    for _ in range(steps):
+        X = rnd(X)
+        Xt = X.mT.contiguous()
+        A = rnd(X @ Xt if wide else Xt @ X)
+        B = rnd(b * A + c * (A @ A))
+        X = a * X + (B @ X if wide else X @ B)
+    return X
+
+
+def orth64(G, steps=5):
+    return iterate(G, steps, lambda x: x)
+
+
+def orth_error(G, ref, steps=5):
+    """Per matrix: twice the largest error norm of four realisations of 11-bit roundings."""
+    def to11(c):
+        def rnd(x):
+            m, e = torch.frexp(x * c)
+            return torch.ldexp(torch.round(m * 2048.0) / 2048.0, e) / c
+        return rnd
+    worst = [torch.linalg.matrix_norm(iterate(G, steps, to11(c)) - ref) for c in (1.0, 1.19, 1.41, 1.68)]
+    return 2.0 * torch.stack(worst).amax(0)
+
+
+def check_orth(got, G, h=0.0, steps=5):
+    """Each matrix of the batch within the bounds of the module's docstring."""
+    ref = orth64(G, steps)
+    for o, r, err in zip(got.double(), ref, orth_error(G, ref, steps).tolist()):
+        assert float((o - r).norm()) <= err + h * float(r.norm()), (float((o - r).norm()), err)
+        assert bool(((o - r).abs() <= 8 * err / math.sqrt(r.numel()) + h * r.abs()).all())
+
+
+SHAPES = [(1, 1, 1), (1, 1, 7), (1, 9, 1), (2, 5, 3), (3, 16, 40), (1, 64, 64), (3, 130, 70), (2, 33, 257),
+          (1, 128, 128), (1, 256, 256), (2, 300, 1001), (2, 515, 300), (1, 129, 2056), (1, 1024, 1024),
+          (1, 2050, 515), (9, 256, 512), (150, 40, 48)]
+
+
+@pytest.mark.parametrize("gtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_orth_matches_float64(shape, gtype):
+    G = place(gradient(shape, sum(shape)).to(TYPES[gtype]))
+    out = place(torch.full(shape, float("nan"), dtype=torch.bfloat16 if gtype == "f32" else torch.float16))
+    lb.muon_orth(G, out)
+    torch.cuda.synchronize()
+    check_guards(out)
+    check_orth(out, G, H[out.dtype])
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("shape", [(2, 40, 64), (1, 130, 72), (3, 64, 37)])
+def test_orth_unaligned(shape, offset):
+    G = place(gradient(shape, 5), offset)
+    out = place(torch.full(shape, float("nan"), dtype=torch.bfloat16), offset)
+    lb.muon_orth(G, out)
+    torch.cuda.synchronize()
+    check_guards(out)
+    check_orth(out, G, H[out.dtype])
+
+
+@pytest.mark.parametrize("steps", [1, 2, 3, 12])
+def test_steps(steps):
+    G = gradient((2, 96, 160), 6).to(DEV)
+    got = lb.muon_orth(G, dtype=torch.float16, steps=steps)
+    check_orth(got, G, H[torch.float16], steps)
+    # the singular values stay in the polynomial's range however many steps run
+    assert float(torch.linalg.matrix_norm(got.double(), 2).max()) <= 1.21 + 1e-2
+
+
+@pytest.mark.parametrize("std", [1e-30, 1e-12, 1.0, 1e18, 1e30])
+def test_any_scale(std):
+    """The norm is summed in float64: squares may leave float32's range."""
+    G = gradient((1, 70, 64), 7, 1.0).to(DEV) * std
+    check_orth(lb.muon_orth(G, dtype=torch.float16), G, H[torch.float16])
+
+
+def test_orthogonal_input_and_zeros_and_nan_stay_apart():
+    q = torch.linalg.qr(torch.randn(128, 128, generator=torch.Generator().manual_seed(1), dtype=torch.float64))[0]
+    G = torch.stack([q.float(), torch.zeros(128, 128), q.float(), torch.randn(128, 128), q.float()]).to(DEV)
+    G[2, 3, 4] = float("nan")
+    G[4, 0, 0] = float("inf")
+    out = lb.muon_orth(G)
+    assert bool((out[1] == 0).all())
+    assert bool(out[2].isnan().all()) and bool(out[4].isnan().all())
+    check_orth(out[[0, 3]], G[[0, 3]], H[out.dtype])
+
+
+def test_batch_is_the_matrices_one_by_one():
+    G = gradient((4, 136, 200), 9).to(DEV)
+    whole = lb.muon_orth(G)
+    for i in range(4):
+        assert torch.equal(whole[i], lb.muon_orth(G[i]))
+
+
+def test_empty():
+    for shape in ((0, 8, 8), (2, 0, 8), (2, 8, 0)):
+        G = torch.empty(shape, device=DEV)
+        assert lb.muon_orth(G).shape == G.shape
+
+
+@pytest.mark.parametrize("shape", [(1, 256, 512), (3, 200, 72), (1, 1100, 1300)])
+def test_repeatable_bit_for_bit(shape):
+    G = gradient(shape, 10).to(DEV)
+    assert torch.equal(lb.muon_orth(G), lb.muon_orth(G))
+
+
+# ---- the update ------------------------------------------------------------------------
+LR, BETA, WD = 3e-4, 0.95, 0.1
+
+
+def step64(W, grad, mom, scale, nesterov=True, inv_scale=1.0, clip=1.0, steps=5):
+    g = grad.double() * inv_scale * clip
+    m = BETA * mom.double() + g
+    o = orth64(g + BETA * m if nesterov else m, steps)
+    u = g + BETA * m if nesterov else m
+    return W.double() - LR * (scale * o + WD * W.double()), m, o, orth_error(u, o, steps)
+
+
+def check_step(W, mom, W0, grad, mom0, scale, **kw):
+    rW, rm, o, err = step64(W0, grad, mom0, scale, **kw)
+    u = 2.0 ** -24
+    g = grad.double().abs() * kw.get("inv_scale", 1.0) * kw.get("clip", 1.0)
+    assert bool(((mom.double() - rm).abs() <= 3 * u * (BETA * mom0.double().abs() + 2 * g) + 1e-44).all())
+    for w, r, w0, oo, e in zip(W.double(), rW, W0.double(), o, err.tolist()):
+        # the orthogonalised update's error, then four fp32 roundings of the update and one of W
+        b = LR * scale * 8 * e / math.sqrt(oo.numel()) + 6 * u * (LR * (scale * oo.abs() + WD * w0.abs()) + w0.abs())
+        assert bool(((w - r).abs() <= b).all())
+        assert float((w - r).norm()) <= LR * scale * e + 2 * u * float(r.norm())
+
+
+def make(shape, gtype, seed, offset=0):
+    g = torch.Generator().manual_seed(seed)
+    W = place(torch.randn(shape, generator=g) * 0.02, offset)
+    grad = place((gradient(shape, seed + 1) * 1024).to(TYPES[gtype]), offset)
+    mom = place(gradient(shape, seed + 2) * 3, offset)
+    return W, grad, mom
+
+
+@pytest.mark.parametrize("gtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 5, 3), (1, 64, 40), (3, 130, 70), (2, 33, 257), (1, 512, 264),
+                                   (1, 1024, 1536), (12, 256, 256)])
+@pytest.mark.parametrize("nesterov", [True, False])
+def test_step_matches_float64(shape, gtype, nesterov):
+    W, grad, mom = make(shape, gtype, 11)
+    W0, m0 = W.clone(), mom.clone()
+    w16 = place(torch.full(shape, float("nan"), dtype=torch.bfloat16 if nesterov else torch.float16))
+    scale = 0.2 * math.sqrt(max(shape[1:]))
+    lb.muon_step(W, grad, mom, LR, BETA, WD, nesterov=nesterov, inv_scale=1 / 1024, w16=w16)
+    torch.cuda.synchronize()
+    for v in (W, mom, w16, grad):
+        check_guards(v)
+    check_step(W, mom, W0, grad, m0, scale, nesterov=nesterov, inv_scale=1 / 1024)
+    assert torch.equal(w16, W.to(w16.dtype))
+
+
+@pytest.mark.parametrize("offset", [1, 2])
+@pytest.mark.parametrize("shape", [(2, 64, 40), (1, 130, 71)])
+def test_step_unaligned(shape, offset):
+    W, grad, mom = make(shape, "bf16", 12, offset)
+    W0, m0 = W.clone(), mom.clone()
+    w16 = place(torch.zeros(shape, dtype=torch.bfloat16), offset)
+    lb.muon_step(W, grad, mom, LR, BETA, WD, scale=2.0, inv_scale=1 / 1024, w16=w16)
+    torch.cuda.synchronize()
+    for v in (W, mom, w16):
+        check_guards(v)
+    check_step(W, mom, W0, grad, m0, 2.0, inv_scale=1 / 1024)
+    assert torch.equal(w16, W.to(torch.bfloat16))
+
+
+def test_clip_and_skip_on_the_device():
+    shape = (2, 72, 136)
+    W, grad, mom = make(shape, "f16", 13)
+    W0, m0 = W.clone(), mom.clone()
+    norm = float((grad.double() / 1024).norm())
+    out, found = lb.grad_norm(grad, 1 / 1024, norm / 2)
+    lb.muon_step(W, grad, mom, LR, BETA, WD, scale=1.0, inv_scale=1 / 1024, clip=out[1:], skip=found)
+    check_step(W, mom, W0, grad, m0, 1.0, inv_scale=1 / 1024, clip=float(out[1]))
+    grad[1, 3, 4] = float("inf")
+    out, found = lb.grad_norm(grad, 1 / 1024, norm / 2)
+    W1, m1 = W.clone(), mom.clone()
+    w16 = place(torch.full(shape, 5.0, dtype=torch.bfloat16))
+    lb.muon_step(W, grad, mom, LR, BETA, WD, scale=1.0, inv_scale=1 / 1024, clip=out[1:], skip=found, w16=w16)
+    assert int(found) == 1 and torch.equal(W, W1) and torch.equal(mom, m1) and bool((w16 == 5.0).all())
+
+
+def test_zero_gradient_only_decays():
+    W, grad, mom = make((1, 64, 64), "f32", 14)
+    grad.zero_()
+    mom.zero_()
+    W0 = W.clone()
+    lb.muon_step(W, grad, mom, LR, BETA, WD)
+    ref = W0.double() * (1 - LR * WD)
+    assert bool(((W.double() - ref).abs() <= 2.0 ** -23 * W0.double().abs()).all()) and bool((mom == 0).all())
+
+
+@pytest.mark.parametrize("shape", [(1, 96, 160), (2, 200, 128)])
+def test_captured_graph_replays(shape):
+    W, grad, mom = make(shape, "bf16", 15)
+    ws = torch.empty(lb.muon_workspace(*shape), dtype=torch.uint8, device=DEV)
+    args = dict(scale=1.0, inv_scale=1 / 1024, ws=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    W0, m0 = W.clone(), mom.clone()
+    with torch.cuda.stream(side):
+        lb.muon_step(W, grad, mom, LR, BETA, WD, **args)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lb.muon_step(W, grad, mom, LR, BETA, WD, **args)
+    W.copy_(W0)
+    mom.copy_(m0)
+    for i in range(4):
+        grad.copy_((gradient(shape, 40 + i) * 1024).to(torch.bfloat16))
+        We, me = W.clone(), mom.clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        lb.muon_step(We, grad, me, LR, BETA, WD, scale=1.0, inv_scale=1 / 1024)
+        torch.cuda.synchronize()
+        assert torch.equal(We, W) and torch.equal(me, mom)
+
+
+def test_two_streams_at_once():
+    cases = [gradient((1, 300, 420), s).to(DEV) for s in (50, 51)]
+    want = [lb.muon_orth(c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        got = []
+        for c, st in zip(cases, streams):
+            with torch.cuda.stream(st):
+                got.append(lb.muon_orth(c))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert torch.equal(a, b)
+
+
+def test_training_step_from_loss_to_update():
+    """The head's loss and gradients, the Linear below it through lin_bwd, Muon for that
+    layer and AdamW for the head, each stage against float64 on the stage's own inputs."""
+    M, D, K, V = 200, 96, 160, 1003
+    g = torch.Generator().manual_seed(60)
+    x = torch.randn(M, D, generator=g).to(DEV, torch.bfloat16)
+    Wl = (torch.randn(D, K, generator=g) * 0.1).to(DEV)
+    Wh = (torch.randn(K, V, generator=g) * 0.05).to(DEV)
+    t = torch.randint(0, V, (M,), generator=g).to(DEV)
+    t[:13] = -100
+    wl, wh = Wl.to(torch.bfloat16), Wh.to(torch.bfloat16)
+    hid = (x.float() @ wl.float()).to(torch.bfloat16)
+    loss, lse, out = lb.lin_xent(hid, wh, t)
+    dh, dwh = torch.empty_like(hid), torch.empty_like(wh)
+    lb.lin_xent_bwd(hid, wh, t, lse, dh, dwh, scale=1024.0, d_scale=out[1:])
+    dwl = torch.empty(D, K, device=DEV)
+    lb.lin_bwd(x, wl, dh, None, dwl)
+    norm, found = lb.grad_norm(dwl, 1 / 1024, 0.01)
+    mom = torch.zeros_like(Wl)
+    W0 = Wl.clone()
+    lb.muon_step(Wl, dwl, mom, LR, BETA, WD, inv_scale=1 / 1024, clip=norm[1:], skip=found, w16=wl)
+    m, v = torch.zeros_like(Wh), torch.zeros_like(Wh)
+    Wh0 = Wh.clone()
+    lb.adamw_step_ex(Wh, dwh, m, v, 1e-3, 0.9, 0.95, 1e-8, WD, 1, 1 / 1024, skip=found, w16=wh)
+    torch.cuda.synchronize()
+
+    hd = hid.double().requires_grad_()
+    wd = Wh0.to(torch.bfloat16).double().requires_grad_()
+    z = hd @ wd
+    keep = t >= 0
+    ref = (torch.logsumexp(z, 1) - z.gather(1, t.clamp(min=0)[:, None])[:, 0])[keep].mean()
+    ref.backward()
+    assert abs(float(out[0]) - float(ref)) <= 1e-5 * float(ref)
+    for a, b in ((dh, hd.grad), (dwh, wd.grad)):   # two bf16 roundings of the gradient, in the mean square
+        assert float((a.double() / 1024 - b).norm()) <= 2 * 2.0 ** -8 * float(b.norm())
+    rw = x.double().T @ dh.double()
+    assert float((dwl.double() - rw).norm()) <= 1e-5 * float(rw.norm())
+    assert int(found) == 0
+    clip = min(1.0, 0.01 / float((dwl.double() / 1024).norm()))
+    rW, _, o, err = step64(W0[None], dwl[None], torch.zeros_like(W0)[None], 0.2 * math.sqrt(K),
+                      inv_scale=1 / 1024, clip=clip)
+    assert float((Wl.double() - rW[0]).norm()) <= LR * 0.2 * math.sqrt(K) * float(err) + 1e-6 * float(rW.norm())
+    assert torch.equal(wl, Wl.to(torch.bfloat16)) and torch.equal(wh, Wh.to(torch.bfloat16))
+    gh = dwh.double() / 1024
+    step = 1e-3 * (gh / (gh.abs() + 1e-8) + WD * Wh0.double())
+    assert bool(((Wh0.double() - Wh.double() - step).abs() <= 1e-8 + 1e-5 * step.abs()).all())
