@@ -130,7 +130,10 @@ __global__ __launch_bounds__(256) void k_muon_scale(PrepParams p) {
     if (p.skip && *p.skip)
         return;
     __shared__ double sh[256];
-    sh[threadIdx.x] = (int)threadIdx.x < p.parts ? p.part[(int64_t)blockIdx.y * p.parts + threadIdx.x] : 0.0;
+    double mine = 0.0;
+    for (int i = threadIdx.x; i < p.parts; i += 256)
+        mine += p.part[(int64_t)blockIdx.y * p.parts + i];
+    sh[threadIdx.x] = mine;
     __syncthreads();
     for (int h = 128; h > 0; h >>= 1) {
         if ((int)threadIdx.x < h)
@@ -194,120 +197,204 @@ struct ProductParams {
     const int32_t *skip;
 };
 
-// VEC: rows of the caller's matrices take 4 elements at a time.
-template <class C, int STEP, bool VEC>
-__global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_muon_product(ProductParams p) {
-    if (p.skip && *p.skip)
-        return;
-    __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
-    LB_LDS char *smem = (LB_LDS char *)smem_raw;
-    const int64_t b = blockIdx.y;
-    Job job = p.job;
-    job.a += b * p.step_a;
-    job.b += b * p.step_b;
-    int ti, tj;
-    coords(job, blockIdx.x, ti, tj);
-    Acc<C> acc;
-    accumulate<C>(job, ti, tj, smem, acc);
-    const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
-    const int64_t I = job.I, J = job.J, Jp = (J + 7) / 8 * 8;
-    const uint16_t *const add = p.add + b * p.step_add;
-    uint16_t *const out = p.out + b * p.step_out;
-    const int64_t mine = b * I * J;
-    staged<C>(acc, i0, j0, smem, [&](int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
-        u32x2_t x[C::FJ];
-        f32x4_t w[C::FJ];
-        if constexpr (STEP != GRAM) {
+__device__ __forceinline__ f32x4_t f16x4(const u32x2_t &h) {
+    return f32x4_t{F16::f32(h[0]), F16::f32(h[0] >> 16), F16::f32(h[1]), F16::f32(h[1] >> 16)};
+}
+
+// GRAM and the ADD that makes B are symmetric (SYM): only the tiles on and below
+// the diagonal run, and each stores its mirror image too.  What is added is loaded one
+// round of the epilogue ahead (the first before the main loop): with the loads in the
+// round that uses them, A² at 4096 took 120 us.
+template <class C, int STEP, bool SYM>
+__device__ __forceinline__ void store_small(const ProductParams &p, const Job &job, int ti, int tj, LB_LDS char *smem) {
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t I = job.I, Jp = (job.J + 7) / 8 * 8;
+    const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
+    const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
+    const uint16_t *const add = p.add + blockIdx.y * p.step_add;
+    uint16_t *const out = p.out + blockIdx.y * p.step_out;
+    u32x2_t next[2][C::FJ], cur[2][C::FJ];
+    auto load = [&](int h) {
+        if constexpr (STEP == ADD) {
 #pragma unroll
-            for (int q = 0; q < C::FJ; ++q) {
-                const int64_t r = i + q * rows;
-                const bool in = r < I && j < Jp;
-                x[q] = in ? *reinterpret_cast<const u32x2_t *>(add + r * p.ld_add + j) : u32x2_t{};
-                if constexpr (STEP == UPDATE && VEC)
-                    w[q] = r < I && j < J ? *reinterpret_cast<const f32x4_t *>(p.W + mine + r * J + j) : f32x4_t{};
+            for (int xx = 0; xx < 2; ++xx) {
+                const int64_t i = ib + 32 * h + 16 * xx + (lane & 15);
+#pragma unroll
+                for (int y = 0; y < C::FJ; ++y) {
+                    const int64_t j = jb + 16 * y + 4 * (lane >> 4);
+                    next[xx][y] = i < I && j < Jp ? *reinterpret_cast<const u32x2_t *>(add + i * p.ld_add + j)
+                                                  : u32x2_t{};
+                }
             }
         }
+    };
+    load(0);
+    Acc<C> acc;
+    accumulate<C>(job, ti, tj, smem, acc);
+    const bool mirror = SYM && ti != tj;
+    store16<C>(
+        acc, out, p.ld_out, I, Jp, ib, jb, true, smem,
+        [&](int h) {
 #pragma unroll
-        for (int q = 0; q < C::FJ; ++q) {
-            const int64_t r = i + q * rows;
+            for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+                for (int y = 0; y < C::FJ; ++y)
+                    cur[xx][y] = next[xx][y];
+            if (h + 1 < C::FI / 2)
+                load(h + 1);
+        },
+        [&](int x, int y) {
             f32x4_t t;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                t[e] = p.f * v[q][e];
-            if constexpr (STEP != GRAM) {
-                const float a[4] = {F16::f32(x[q][0]), F16::f32(x[q][0] >> 16), F16::f32(x[q][1]),
-                                    F16::f32(x[q][1] >> 16)};
+                t[e] = p.f * acc[x][y][e];
+            if constexpr (STEP == ADD) {
+                const f32x4_t a = f16x4(cur[x & 1][y]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     t[e] = __builtin_fmaf(p.fa, a[e], t[e]);
             }
-            if (r >= I)
-                continue;
-            if constexpr (STEP == GRAM || STEP == ADD) {
-                if (j < Jp)
-                    *reinterpret_cast<u32x2_t *>(out + r * p.ld_out + j) =
-                        u32x2_t{F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
-            } else if constexpr (STEP == ORTH) {
-                uint16_t h[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    h[e] = p.o_bf16 ? BF16::one(t[e]) : F16::one(t[e]);
-                uint16_t *const o = p.o + mine + r * J + j;
-                if constexpr (VEC) {
-                    if (j < J)
-                        *reinterpret_cast<u32x2_t *>(o) =
-                            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
-                } else {
+            const u32x2_t h = {F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
+            if (mirror) { // 16 lanes of one column: 32 bytes of a row of the mirror image
+                const int64_t i = ib + 16 * x + (lane & 15), j = jb + 16 * y + 4 * (lane >> 4);
+                if (i < Jp) // the padding columns too (zero)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (j + e < J)
-                            o[e] = h[e];
-                }
-            } else {
-                const int64_t at = mine + r * J + j;
-                auto stepped = [&](float old, float o) { return old - p.lr * (p.scale * o + p.wd * old); };
-                if constexpr (VEC) {
-                    if (j >= J)
-                        continue;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[q][e] = stepped(w[q][e], t[e]);
-                    *reinterpret_cast<f32x4_t *>(p.W + at) = w[q];
-                    if (p.W16)
-                        *reinterpret_cast<u32x2_t *>(p.W16 + at) =
-                            p.o_bf16 ? u32x2_t{BF16::pack2(w[q][0], w[q][1]), BF16::pack2(w[q][2], w[q][3])}
-                                     : u32x2_t{F16::pack2(w[q][0], w[q][1]), F16::pack2(w[q][2], w[q][3])};
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < J) {
-                            const float nw = stepped(p.W[at + e], t[e]);
-                            p.W[at + e] = nw;
-                            if (p.W16)
-                                p.W16[at + e] = p.o_bf16 ? BF16::one(nw) : F16::one(nw);
-                        }
-                }
+                        if (j + e < I)
+                            out[(j + e) * p.ld_out + i] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
             }
-        }
-    });
+            return h;
+        });
 }
 
+// The last product, on the caller's matrices.  VEC: their rows take 4 elements at a time.
 template <class C, int STEP, bool VEC>
+__device__ __forceinline__ void store_last(const ProductParams &p, const Job &job, int ti, int tj, LB_LDS char *smem) {
+    Acc<C> acc;
+    accumulate<C>(job, ti, tj, smem, acc);
+    const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
+    const int64_t I = job.I, J = job.J;
+    const uint16_t *const add = p.add + blockIdx.y * p.step_add; // ld a multiple of 8, padded
+    const int64_t mine = blockIdx.y * I * J;
+    u32x2_t x[C::FJ];
+    f32x4_t w[C::FJ];
+    auto load = [&](int64_t i, int rows, int64_t j) {
+#pragma unroll
+        for (int q = 0; q < C::FJ; ++q) {
+            const int64_t r = i + q * rows;
+            const bool in = r < I && j < J;
+            x[q] = in ? *reinterpret_cast<const u32x2_t *>(add + r * p.ld_add + j) : u32x2_t{};
+            if constexpr (STEP == UPDATE && VEC)
+                w[q] = in ? *reinterpret_cast<const f32x4_t *>(p.W + mine + r * J + j) : f32x4_t{};
+        }
+    };
+    staged<C>(
+        acc, i0, j0, smem,
+        [&](int, int64_t i, int rows, int64_t j) {
+            load(i, rows, j);
+        },
+        [&](int, int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
+#pragma unroll
+            for (int q = 0; q < C::FJ; ++q) {
+                const int64_t r = i + q * rows;
+                if (r >= I || j >= J)
+                    continue;
+                const f32x4_t a = f16x4(x[q]);
+                f32x4_t t;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    t[e] = __builtin_fmaf(p.fa, a[e], p.f * v[q][e]);
+                const int64_t at = mine + r * J + j;
+                if constexpr (STEP == ORTH) {
+                    uint16_t h[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        h[e] = p.o_bf16 ? BF16::one(t[e]) : F16::one(t[e]);
+                    if constexpr (VEC) {
+                        *reinterpret_cast<u32x2_t *>(p.o + at) =
+                            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e < J)
+                                p.o[at + e] = h[e];
+                    }
+                } else {
+                    auto stepped = [&](float old, float o) { return old - p.lr * (p.scale * o + p.wd * old); };
+                    if constexpr (VEC) {
+                        f32x4_t n;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            n[e] = stepped(w[q][e], t[e]);
+                        *reinterpret_cast<f32x4_t *>(p.W + at) = n;
+                        if (p.W16)
+                            *reinterpret_cast<u32x2_t *>(p.W16 + at) =
+                                p.o_bf16 ? u32x2_t{BF16::pack2(n[0], n[1]), BF16::pack2(n[2], n[3])}
+                                         : u32x2_t{F16::pack2(n[0], n[1]), F16::pack2(n[2], n[3])};
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (j + e < J) {
+                                const float n = stepped(p.W[at + e], t[e]);
+                                p.W[at + e] = n;
+                                if (p.W16)
+                                    p.W16[at + e] = p.o_bf16 ? BF16::one(n) : F16::one(n);
+                            }
+                    }
+                }
+            }
+        });
+}
+
+// FLAG: SYM of GRAM and ADD, VEC of ORTH and UPDATE.
+template <class C, int STEP, bool FLAG>
+__global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_product(ProductParams p) {
+    if (p.skip && *p.skip)
+        return;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
+    LB_LDS char *smem = (LB_LDS char *)smem_raw;
+    Job job = p.job;
+    job.a += blockIdx.y * p.step_a;
+    job.b += blockIdx.y * p.step_b;
+    int ti, tj;
+    if constexpr ((STEP == GRAM || STEP == ADD) && FLAG)
+        coords_lower(job.tiles_i, blockIdx.x, ti, tj);
+    else
+        coords(job, blockIdx.x, ti, tj);
+    if constexpr (STEP == GRAM || STEP == ADD)
+        store_small<C, STEP, FLAG>(p, job, ti, tj, smem);
+    else
+        store_last<C, STEP, FLAG>(p, job, ti, tj, smem);
+}
+
+template <class C, int STEP, bool FLAG>
 void launch(ProductParams &p, int64_t batch, hipStream_t s) {
     p.job.tiles_i = (int)cdiv(p.job.I, C::TI);
     p.job.tiles_j = (int)cdiv(p.job.J, C::TJ);
     p.job.group = 4;
-    hipLaunchKernelGGL((k_muon_product<C, STEP, VEC>), dim3((unsigned)(p.job.tiles_i * p.job.tiles_j), (unsigned)batch),
-                       dim3(kThreads), 0, s, p);
+    const int64_t tiles = (STEP == GRAM || STEP == ADD) && FLAG
+                              ? (int64_t)p.job.tiles_i * (p.job.tiles_i + 1) / 2
+                              : (int64_t)p.job.tiles_i * p.job.tiles_j;
+    hipLaunchKernelGGL((k_muon_product<C, STEP, FLAG>), dim3((unsigned)tiles, (unsigned)batch), dim3(kThreads), 0, s,
+                       p);
 }
-template <bool AOC, bool BOC, int STEP, bool VEC = true>
+template <bool AOC, bool BOC, int STEP, bool FLAG>
 void product(ProductParams &p, int64_t batch, hipStream_t s) {
-    if (muon::big_tiles(batch, p.job.I, p.job.J))
-        launch<Cfg<F16, 2, 2, 8, 8, AOC, BOC, 2>, STEP, VEC>(p, batch, s);
-    else
-        launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 2>, STEP, VEC>(p, batch, s);
+    const bool sym = (STEP == GRAM || STEP == ADD) && FLAG;
+    switch (muon::choose(batch, p.job.I, p.job.J, sym)) {
+    case muon::TILE256: launch<Cfg<F16, 2, 2, 8, 8, AOC, BOC, 2, 3>, STEP, FLAG>(p, batch, s); break;
+    case muon::TILE128: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 2>, STEP, FLAG>(p, batch, s); break;
+    default: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
+    }
 }
-// the last product, on the caller's matrices
+template <bool AOC, bool BOC, int STEP>
+void symmetric_product(ProductParams &p, int64_t batch, hipStream_t s) {
+    if (muon::lower_only(batch, p.job.I))
+        product<AOC, BOC, STEP, true>(p, batch, s);
+    else
+        product<AOC, BOC, STEP, false>(p, batch, s);
+}
 template <int STEP>
 void last_product(ProductParams &p, int64_t batch, bool tall, bool vec, hipStream_t s) {
     if (tall)
@@ -387,10 +474,10 @@ hipError_t launch_muon(const MuonArgs &a, hipStream_t s) {
     for (int t = 0; t < a.steps; ++t) {
         gram.job.a = gram.job.b = x;
         if (pl.tall)
-            product<true, true, GRAM>(gram, a.batch, s);
+            symmetric_product<true, true, GRAM>(gram, a.batch, s);
         else
-            product<false, false, GRAM>(gram, a.batch, s);
-        product<false, false, ADD>(poly, a.batch, s);
+            symmetric_product<false, false, GRAM>(gram, a.batch, s);
+        symmetric_product<false, false, ADD>(poly, a.batch, s);
         const bool last = t + 1 == a.steps;
         upd.job.a = pl.tall ? x : gb;
         upd.job.b = pl.tall ? gb : x;
@@ -400,7 +487,8 @@ hipError_t launch_muon(const MuonArgs &a, hipStream_t s) {
         upd.f = last ? 1.0f / (kX * kG) : 1.0f / kG;
         upd.fa = last ? kA / kX : kA;
         if (!last)
-            pl.tall ? product<false, false, ADD>(upd, a.batch, s) : product<false, true, ADD>(upd, a.batch, s);
+            pl.tall ? product<false, false, ADD, false>(upd, a.batch, s)
+                    : product<false, true, ADD, false>(upd, a.batch, s);
         else if (a.W)
             last_product<UPDATE>(upd, a.batch, pl.tall, rows4, s);
         else

@@ -21,8 +21,9 @@ inline int tile_cols(int r) { return r == ROWS256 ? 256 : 128; }
 inline int choose_rows(int64_t M) { return M <= 32 ? ROWS32 : M <= 64 ? ROWS64 : M <= 128 ? ROWS128 : ROWS256; }
 
 // A packed copy of W's piece (V not a multiple of 8, or W not 16-byte aligned) takes at
-// most this; the piece is then read from the caches by the products that follow.
-constexpr int64_t kPackBytes = (int64_t)128 << 20;
+// most this.  Large pieces waste fewer part-filled rounds of tiles (pieces of 128 MiB,
+// which stay in the last-level cache, were slower).
+constexpr int64_t kPackBytes = (int64_t)1 << 30;
 // per-tile softmax statistics of a forward piece
 constexpr int64_t kPartBytes = (int64_t)128 << 20;
 // the piece of dL/dlogits (16 bit) that the backward pass holds
@@ -41,21 +42,24 @@ struct Fwd {
     int rows;          // Rows
     int64_t Kp;        // K rounded up to 8
     int64_t Vc;        // piece width
-    int64_t wcols;     // columns per statistics entry (one wave's)
-    int64_t parts;     // entries per row and piece
-    int64_t off_x, off_w, off_part, off_run, off_zt, bytes;
+    int64_t parts;     // statistics entries (tiles) per row and piece
+    int join_rows;     // rows per block that joins them
+    int64_t off_x, off_w, off_part, off_run, off_zt, off_sum, bytes;
 };
 
 inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     Fwd f;
     f.rows = choose_rows(M);
     f.Kp = up(K, 8);
-    f.wcols = f.rows == ROWS256 ? 128 : f.rows == ROWS128 ? 64 : 32;
-    // statistics: 8 bytes per row and wcols columns
-    f.Vc = piece(V, cdiv(8 * M, f.wcols), kPartBytes);
+    const int64_t cols = tile_cols(f.rows);
+    f.Vc = piece(V, cdiv(8 * M, cols), kPartBytes);
     if (pack_w)
         f.Vc = std::min(f.Vc, piece(V, 2 * K, kPackBytes));
-    f.parts = up(f.Vc, tile_cols(f.rows)) / f.wcols;
+    f.parts = cdiv(f.Vc, cols);
+    f.join_rows = M <= 4096 ? 16 : 64;
+    if (M <= 32)
+        for (f.join_rows = 1; f.join_rows < M;)
+            f.join_rows *= 2;
     int64_t at = 0;
     auto take = [&](int64_t n) {
         const int64_t o = at;
@@ -67,6 +71,7 @@ inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     f.off_part = take(8 * M * f.parts);
     f.off_run = take(8 * M);
     f.off_zt = take(4 * M);
+    f.off_sum = take(16 * cdiv(M, f.join_rows));
     f.bytes = at;
     return f;
 }

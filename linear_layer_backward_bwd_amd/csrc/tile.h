@@ -66,16 +66,16 @@ struct F16 {
     }
 };
 
-// Four waves as WI x WJ, each FI x FJ fragments of 16 x 16; S pair slots.
-template <class T_, int WI_, int WJ_, int FI_, int FJ_, bool AOC_, bool BOC_, int S_>
+// Four waves as WI x WJ, each FI x FJ fragments of 16 x 16; S pair slots for A, SB for B.
+template <class T_, int WI_, int WJ_, int FI_, int FJ_, bool AOC_, bool BOC_, int S_, int SB_ = S_>
 struct Cfg {
     using T = T_;
-    static constexpr int WI = WI_, WJ = WJ_, FI = FI_, FJ = FJ_, S = S_;
+    static constexpr int WI = WI_, WJ = WJ_, FI = FI_, FJ = FJ_, S = S_, SB = SB_;
     static constexpr bool AOC = AOC_, BOC = BOC_;
     static constexpr int TI = WI * FI * 16, TJ = WJ * FJ * 16;
     static constexpr int kPairA = TI * 128, kPairB = TJ * 128; // bytes of an operand's pair
     static constexpr int kOffB = S * kPairA;                   // A's slots first, then B's
-    static constexpr int kLds = S * (kPairA + kPairB);
+    static constexpr int kLds = S * kPairA + SB * kPairB;
     static constexpr int kDmaA = TI / 32, kDmaB = TJ / 32; // DMA instructions per wave per pair
     static constexpr int kDma = kDmaA + kDmaB;
     static_assert(WI * WJ == 4, "four waves");
@@ -83,7 +83,9 @@ struct Cfg {
     static_assert(!AOC || TI == 128 || TI == 256, "OC rows of 256 or 512 bytes");
     static_assert(!BOC || TJ == 128 || TJ == 256, "OC rows of 256 or 512 bytes");
     static_assert(4 * FJ * 1024 <= kLds, "the epilogue stages 16 rows per wave in the ring");
-    static_assert((S - 2) * kDma < 64, "vmcnt is 6 bits");
+    // DMA instructions that may be in flight while the next pair has landed
+    static constexpr int kAhead = (S - 2) * kDma + (SB - S) * kDmaB;
+    static_assert(SB >= S && kAhead + kDma < 64, "vmcnt is 6 bits");
 };
 
 // One product.  lda, ldb multiples of 8 elements, a and b 16-byte aligned.  Operands are
@@ -130,6 +132,21 @@ __device__ __forceinline__ void coords(const Job &jb, int t, int &ti, int &tj) {
     u -= g * per;
     ti = first + u % rows;
     tj = u / rows;
+}
+
+// The same for a symmetric product: the tiles on and below the diagonal only (tj <= ti),
+// row by row.
+__device__ __forceinline__ void coords_lower(int tiles, int t, int &ti, int &tj) {
+    const int n = tiles * (tiles + 1) / 2;
+    const int x = t & 7, rem = n & 7;
+    const int u = x * (n >> 3) + (x < rem ? x : rem) + (t >> 3);
+    ti = (int)((__builtin_sqrtf(8.0f * (float)u + 1.0f) - 1.0f) * 0.5f);
+    while (ti * (ti + 1) / 2 > u)
+        --ti;
+    while ((ti + 1) * (ti + 2) / 2 <= u)
+        ++ti;
+    ti = __builtin_amdgcn_readfirstlane(ti);
+    tj = u - ti * (ti + 1) / 2;
 }
 
 // One operand of a tile: T outer indices from o0 on.
@@ -223,7 +240,7 @@ struct Frags {
         }
     }
     // read number k (0..kReads-1) of slab half H; the slot is a compile-time constant
-    // where its offset fits the instruction's 16 bits (S == 2), else SLOT is 0 and `add` holds it
+    // where its offset fits the instruction's 16 bits (two slots), else SLOT is 0 and `add` holds it
     template <int SLOT, int H>
     __device__ __forceinline__ void read(int k, int add, u32x4_t (&f)[F], frag_half_t (&h)[F][2]) const {
         if constexpr (OC) {
@@ -292,9 +309,9 @@ __device__ __forceinline__ void pin(f32x4_t (&a)[N]) {
 template <class C>
 __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS char *smem, Acc<C> &acc) {
     using SA = Side<C::TI, C::AOC, C::kDmaA, C::S>;
-    using SB = Side<C::TJ, C::BOC, C::kDmaB, C::S>;
+    using SB = Side<C::TJ, C::BOC, C::kDmaB, C::SB>;
     using FA = Frags<C::TI, C::AOC, C::FI, C::S>;
-    using FB = Frags<C::TJ, C::BOC, C::FJ, C::S>;
+    using FB = Frags<C::TJ, C::BOC, C::FJ, C::SB>;
     constexpr int FI = C::FI, FJ = C::FJ, NM = FI * FJ;
     constexpr int NR = FA::kReads + FB::kReads;
     const int lane = threadIdx.x & 63;
@@ -318,20 +335,12 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
     u32x4_t a0[FI], b0[FJ], a1[FI], b1[FJ];
     frag_half_t ha[FI][2], hb[FJ][2];
 
-    auto issue = [&](const typename SA::Src &xa, const typename SB::Src &xb, int slot, int d) {
-        // the operands in turn where they have as many instructions
-        int op, k;
-        if constexpr (C::kDmaA == C::kDmaB) {
-            op = d & 1;
-            k = d >> 1;
-        } else {
-            op = d >= C::kDmaA;
-            k = op ? d - C::kDmaA : d;
-        }
-        if (op == 0)
-            sa.dma(xa, smem + slot * C::kPairA, w, k);
+    // DMA instruction d of a pair: A's, then B's (which may have a slot more, and time)
+    auto issue = [&](const typename SA::Src &xa, const typename SB::Src &xb, int slot_a, int slot_b, int d) {
+        if (d < C::kDmaA)
+            sa.dma(xa, smem + slot_a * C::kPairA, w, d);
         else
-            sb.dma(xb, smem + C::kOffB + slot * C::kPairB, w, k);
+            sb.dma(xb, smem + C::kOffB + slot_b * C::kPairB, w, d - C::kDmaA);
     };
     auto settle = [&](u32x4_t (&af)[FI], u32x4_t (&bf)[FJ]) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -341,9 +350,10 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
     };
     // MFMAs of one slab on (af, bf), the LDS reads of slab half H of the pair in slot
     // SLOT (+ adds) into (an, bn) after the first of them, `other(i)` after each
-    auto slab = [&](auto slot_c, auto half_c, int add_a, int add_b, u32x4_t (&af)[FI], u32x4_t (&bf)[FJ],
+    auto slab = [&](auto slot_c, auto slotb_c, auto half_c, int add_a, int add_b, u32x4_t (&af)[FI], u32x4_t (&bf)[FJ],
                     u32x4_t (&an)[FI], u32x4_t (&bn)[FJ], auto other) {
-        constexpr int SLOT = decltype(slot_c)::value, H = decltype(half_c)::value;
+        constexpr int SLOT = decltype(slot_c)::value, SLOTB = decltype(slotb_c)::value;
+        constexpr int H = decltype(half_c)::value;
         constexpr int kPer = (NR + NM - 1) / NM;                             // reads per MFMA
         constexpr int kEvery = NR <= NM ? (NM / 2 / NR > 0 ? NM / 2 / NR : 1) : 1; // MFMAs per read
         __builtin_amdgcn_sched_barrier(0);
@@ -358,7 +368,7 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
                     if (k < FA::kReads)
                         fa.template read<SLOT, H>(k, add_a, an, ha);
                     else if (k < NR)
-                        fb.template read<SLOT, H>(k - FA::kReads, add_b, bn, hb);
+                        fb.template read<SLOTB, H>(k - FA::kReads, add_b, bn, hb);
                 }
             }
             other(i);
@@ -369,16 +379,19 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
     using Z = std::integral_constant<int, 0>;
     using O = std::integral_constant<int, 1>;
 
-    // prologue: S pairs on their way; the first slab's fragments
+    // prologue: every slot on its way; the first slab's fragments
+    typename SA::Src xa;
+    typename SB::Src xb;
 #pragma unroll
-    for (int s = 0; s < C::S; ++s) {
-        const auto xa = sa.next();
-        const auto xb = sb.next();
+    for (int s = 0; s < C::SB; ++s) {
+        if (s < C::S)
+            xa = sa.next();
+        xb = sb.next();
 #pragma unroll
-        for (int d = 0; d < C::kDma; ++d)
-            issue(xa, xb, s, d);
+        for (int d = s < C::S ? 0 : C::kDmaA; d < C::kDma; ++d)
+            issue(xa, xb, s, s, d);
     }
-    vm_wait<(C::S - 1) * C::kDma < 64 ? (C::S - 1) * C::kDma : 63>();
+    vm_wait<C::kAhead + C::kDma>();
     ring_barrier();
 #pragma unroll
     for (int k = 0; k < FA::kReads; ++k)
@@ -388,43 +401,41 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
         fb.template read<0, 0>(k, 0, b0, hb);
     settle(a0, b0);
 
-    // one pair in slot SLOT (S == 2) or `slot`; NEXT: the following pair's slot
-    auto pair = [&](auto slot_c, auto next_c, int slot, int next) {
-        constexpr int SLOT = decltype(slot_c)::value;
-        constexpr bool fixed = C::S == 2;
-        const int aa = fixed ? 0 : slot * C::kPairA, ab = fixed ? 0 : slot * C::kPairB;
-        const int na = fixed ? 0 : next * C::kPairA, nb = fixed ? 0 : next * C::kPairB;
-        typename SA::Src xa;
-        typename SB::Src xb;
-        // first half; the descriptors of the pair S ahead are made between its MFMAs
-        slab(slot_c, O{}, aa, ab, a0, b0, a1, b1, [&](int i) {
+    // One pair.  A slot is a compile-time constant (PAR, of two) or `ia`; so is B's where
+    // both have two, else `ib`.
+    constexpr bool fixa = C::S == 2, fixb = C::S == 2 && C::SB == 2;
+    int ia = 0, ib = 0; // the pair's slots where they are not constants
+    auto pair = [&](auto par, auto next) {
+        using PB = std::integral_constant<int, fixb ? decltype(par)::value : 0>;
+        using NB = std::integral_constant<int, fixb ? decltype(next)::value : 0>;
+        const int ja = ia + 1 == C::S ? 0 : ia + 1, jb = ib + 1 == C::SB ? 0 : ib + 1;
+        // first half; the descriptors of the pairs to fetch are made between its MFMAs
+        slab(par, PB{}, O{}, fixa ? 0 : ia * C::kPairA, fixb ? 0 : ib * C::kPairB, a0, b0, a1, b1, [&](int i) {
             if (i == NM - 2) {
                 xa = sa.next();
                 xb = sb.next();
             }
         });
-        vm_wait<(C::S - 2) * C::kDma>(); // the next pair has landed
-        ring_barrier();                  // everyone's; and this pair's slot is free
-        slab(next_c, Z{}, na, nb, a1, b1, a0, b0, [&](int i) {
+        vm_wait<C::kAhead>(); // the next pair has landed
+        ring_barrier();       // everyone's; and this pair's slots are free
+        slab(next, NB{}, Z{}, fixa ? 0 : ja * C::kPairA, fixb ? 0 : jb * C::kPairB, a1, b1, a0, b0, [&](int i) {
 #pragma unroll
             for (int d = i * C::kDma / NM; d < (i + 1) * C::kDma / NM; ++d)
-                issue(xa, xb, fixed ? SLOT : slot, d);
+                issue(xa, xb, fixa ? decltype(par)::value : ia, fixb ? decltype(par)::value : ib, d);
         });
+        ia = ja;
+        ib = jb;
     };
-    if constexpr (C::S == 2) {
+    if constexpr (fixa) {
         // an odd count runs one pair of zeros more: with an exit between the two the
         // compiler copied the accumulators out of the AGPRs on every turn
         for (int q = 0; q < npair; q += 2) {
-            pair(Z{}, O{}, 0, 1);
-            pair(O{}, Z{}, 1, 0);
+            pair(Z{}, O{});
+            pair(O{}, Z{});
         }
     } else {
-        int slot = 0;
-        for (int q = 0; q < npair; ++q) {
-            const int next = slot + 1 == C::S ? 0 : slot + 1;
-            pair(Z{}, Z{}, slot, next);
-            slot = next;
-        }
+        for (int q = 0; q < npair; ++q)
+            pair(Z{}, Z{});
     }
     mfma_drain();
     vm_wait<0>();
@@ -433,10 +444,12 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
 
 // Passes a wave's sums through its own part of the ring, 16 rows at a time, so that a
 // lane holds 4 consecutive columns and 4*FJ lanes a row's FJ*16 columns (direct from the
-// accumulators a store instruction would touch 16 rows).  round(i, rows, j, v): v[q] is
-// C[i + q*rows][j..j+3], q < FJ.
-template <class C, class Fn>
-__device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_LDS char *smem, Fn round) {
+// accumulators a store instruction would touch 16 rows).  round(x, i, rows, j, v): v[q] is
+// C[i + q*rows][j..j+3], q < FJ; begin(x, i, rows, j) comes before the round's LDS traffic
+// (to load what a later round combines with).
+template <class C, class Begin, class Fn>
+__device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_LDS char *smem, Begin begin,
+                                       Fn round) {
     constexpr int FJ = C::FJ, kChunks = 4 * FJ, kRows = 64 / kChunks;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -444,6 +457,8 @@ __device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_L
     const int64_t ib = i0 + (w / C::WJ) * C::FI * 16, jb = j0 + (w % C::WJ) * FJ * 16;
 #pragma unroll
     for (int x = 0; x < C::FI; ++x) {
+        asm volatile("" ::: "memory"); // loads of later rounds stay behind this one's stores
+        begin(x, ib + 16 * x + lane / kChunks, kRows, jb + 4 * (lane % kChunks));
         pin(acc[x]);
 #pragma unroll
         for (int y = 0; y < FJ; ++y) {
@@ -457,7 +472,63 @@ __device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_L
             v[q] = *reinterpret_cast<const LB_LDS f32x4_t *>(reg + r * (FJ * 64) + ((c ^ (r & (kChunks - 1))) << 4));
         }
         __builtin_amdgcn_sched_barrier(0); // all reads before the first use
-        round(ib + 16 * x + lane / kChunks, kRows, jb + 4 * (lane % kChunks), v);
+        round(x, ib + 16 * x + lane / kChunks, kRows, jb + 4 * (lane % kChunks), v);
+    }
+}
+
+// 16-bit output through LDS: 32 rows of a wave at a time, whole 16-byte chunks per lane.
+// begin(h) is called before round h, value(x, y) gives the 4 packed values of acc[x][y].
+// vec: rows of dst 16-byte aligned and J a multiple of 8.
+template <class C, class Begin, class Fn>
+__device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, int64_t I, int64_t J, int64_t ib, int64_t jb,
+                                        bool vec, LB_LDS char *smem, Begin begin,
+                                        Fn value) {
+    constexpr int FJ = C::FJ, kRowB = FJ * 32, kChunks = 2 * FJ, kRows = 64 / kChunks;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    LB_LDS char *const reg = smem + w * (FJ * 1024);
+#pragma unroll
+    for (int h = 0; h < C::FI / 2; ++h) {
+        asm volatile("" ::: "memory"); // loads of later rounds stay behind this one's stores
+        begin(h);
+        pin(acc[2 * h]);
+        pin(acc[2 * h + 1]);
+#pragma unroll
+        for (int xx = 0; xx < 2; ++xx)
+#pragma unroll
+            for (int y = 0; y < FJ; ++y) {
+                const int r = 16 * xx + (lane & 15);
+                const int c = 2 * y + (lane >> 5); // 16-byte chunk: 8 columns
+                *reinterpret_cast<LB_LDS u32x2_t *>(reg + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4) +
+                                                    ((lane >> 4) & 1) * 8) = value(2 * h + xx, y);
+            }
+        const int64_t i0 = ib + 32 * h;
+        if (vec) {
+            u32x4_t v[FJ];
+#pragma unroll
+            for (int q = 0; q < FJ; ++q) {
+                const int r = q * kRows + lane / kChunks, c = lane % kChunks;
+                v[q] = *reinterpret_cast<const LB_LDS u32x4_t *>(reg + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4));
+            }
+            __builtin_amdgcn_sched_barrier(0); // all reads before the first store
+            const int64_t j = jb + 8 * (lane % kChunks);
+#pragma unroll
+            for (int q = 0; q < FJ; ++q) {
+                const int64_t i = i0 + q * kRows + lane / kChunks;
+                if (i < I && j < J)
+                    __builtin_nontemporal_store(v[q], reinterpret_cast<u32x4_t *>(dst + i * ld + j));
+            }
+        } else {
+            // rows of any alignment: 64 lanes store 64 neighbouring elements
+            for (int q = 0; q < 32 * FJ * 16 / 64; ++q) {
+                const int e = q * 64 + lane;
+                const int r = e / (FJ * 16), c = e % (FJ * 16);
+                const uint16_t v = *reinterpret_cast<const LB_LDS uint16_t *>(
+                    reg + r * kRowB + (((c >> 3) ^ (r & (kChunks - 1))) << 4) + (c & 7) * 2);
+                if (i0 + r < I && jb + c < J)
+                    dst[(i0 + r) * ld + jb + c] = v;
+            }
+        }
     }
 }
 

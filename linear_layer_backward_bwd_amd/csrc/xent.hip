@@ -33,6 +33,8 @@ namespace {
 using namespace tile;
 using xent::cdiv;
 
+typedef float pair_t __attribute__((ext_vector_type(2)));
+
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
@@ -48,17 +50,17 @@ struct RowParam {
 
 // ---- copies: zero-padded rows, 16-byte aligned -----------------------------------------
 // dst [rows, ldd] (ldd % 8 == 0) from src[r*lds + c], c < cols; columns past cols are
-// zero, and so are the rows that `row` (if given) says take no part (their X may hold
-// anything).  One 16-byte chunk per thread; unaligned sources are read as dwords (two
+// zero, and so are rows that `keep` leaves out.  One 16-byte chunk per thread; unaligned sources are read as dwords (two
 // bytes apart: shifted together), the first and last chunk of such a row by elements.
-__global__ __launch_bounds__(256) void k_xent_pack(const uint16_t *src, int64_t lds, int64_t rows, int64_t cols,
-                                                   uint16_t *dst, int64_t ldd, const RowParam *row) {
+template <class Keep>
+__device__ __forceinline__ void pack_rows(const uint16_t *src, int64_t lds, int64_t rows, int64_t cols, uint16_t *dst,
+                                          int64_t ldd, int64_t first, int64_t stride, Keep keep) {
     typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
     const int64_t per = ldd / 8, n = rows * per;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    for (int64_t i = first; i < n; i += stride) {
         const int64_t r = i / per, c = (i - r * per) * 8;
         u32x4_t v = {};
-        if (c < cols && !(row && row[r].t < 0 && row[r].s == 0.0f)) {
+        if (c < cols && keep(r)) {
             const uint16_t *p = src + r * lds + c;
             const uintptr_t a = reinterpret_cast<uintptr_t>(p);
             if (c + 8 <= cols && (a & 15) == 0) {
@@ -81,11 +83,16 @@ __global__ __launch_bounds__(256) void k_xent_pack(const uint16_t *src, int64_t 
     }
 }
 
-void pack(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst, int64_t ldd, const RowParam *row,
-          hipStream_t s) {
+__global__ __launch_bounds__(256) void k_xent_pack(const uint16_t *src, int64_t lds, int64_t rows, int64_t cols,
+                                                   uint16_t *dst, int64_t ldd) {
+    pack_rows(src, lds, rows, cols, dst, ldd, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256,
+              [](int64_t) { return true; });
+}
+
+void pack(const void *src, int64_t lds, int64_t rows, int64_t cols, void *dst, int64_t ldd, hipStream_t s) {
     const int64_t blocks = std::min<int64_t>(cdiv(rows * (ldd / 8), 256), 16 * xent::kCUs);
     hipLaunchKernelGGL(k_xent_pack, dim3((unsigned)blocks), dim3(256), 0, s, static_cast<const uint16_t *>(src), lds,
-                       rows, cols, static_cast<uint16_t *>(dst), ldd, row);
+                       rows, cols, static_cast<uint16_t *>(dst), ldd);
 }
 
 // ---- forward ---------------------------------------------------------------------------
@@ -93,13 +100,19 @@ struct StatsParams {
     Job job;               // A = X (RC), B = W's piece (OC)
     const int64_t *target; // [M]
     int64_t v0;            // first column of the piece
-    float2 *part;          // [parts][M]: (maximum·log2 e, Σ 2^(z·log2 e − that))
+    pair_t *part;          // [tiles][M]: (maximum·log2 e, Σ 2^(z·log2 e − that))
     float *zt;             // [M] target logits
 };
 
+__device__ __forceinline__ pair_t join(pair_t a, pair_t b) {
+    const float m = fmaxf(a.x, b.x);
+    const float r = m == -INFINITY ? 0.0f : m; // nothing yet on either side
+    return pair_t{m, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r)};
+}
+
 template <class C, bool FULL>
 __device__ __forceinline__ void stats_epilogue(const StatsParams &p, Acc<C> &acc, int64_t ib, int64_t jb,
-                                               int64_t slot, int lane) {
+                                               pair_t (&st)[C::FI], int lane) {
     const int64_t M = p.job.I;
 #pragma unroll
     for (int x = 0; x < C::FI; ++x) {
@@ -137,8 +150,7 @@ __device__ __forceinline__ void stats_epilogue(const StatsParams &p, Acc<C> &acc
                     z = ((int)t >> 4) == y && ((int)t & 3) == e ? acc[x][y][e] : z;
             p.zt[i] = z;
         }
-        if (lane < 16 && row)
-            p.part[slot * M + i] = make_float2(mx == -INFINITY ? -INFINITY : m2, s);
+        st[x] = pair_t{mx == -INFINITY ? -INFINITY : m2, s};
     }
 }
 
@@ -154,73 +166,82 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_stats(S
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
-    const int64_t slot = (int64_t)tj * C::WJ + w % C::WJ;
+    pair_t st[C::FI]; // of this wave's columns
     if (jb + C::FJ * 16 <= p.job.J)
-        stats_epilogue<C, true>(p, acc, ib, jb, slot, lane);
+        stats_epilogue<C, true>(p, acc, ib, jb, st, lane);
     else
-        stats_epilogue<C, false>(p, acc, ib, jb, slot, lane);
+        stats_epilogue<C, false>(p, acc, ib, jb, st, lane);
+    // join the waves that hold the same rows
+    LB_LDS pair_t *const sh = (LB_LDS pair_t *)smem; // [WJ][TI]
+#pragma unroll
+    for (int x = 0; x < C::FI; ++x)
+        if (lane < 16)
+            sh[(w % C::WJ) * C::TI + (w / C::WJ) * C::FI * 16 + 16 * x + lane] = st[x];
+    __syncthreads();
+    const int r = threadIdx.x;
+    const int64_t i = (int64_t)ti * C::TI + r;
+    if (r < C::TI && i < p.job.I) {
+        pair_t a = sh[r];
+#pragma unroll
+        for (int k = 1; k < C::WJ; ++k)
+            a = join(a, sh[k * C::TI + r]);
+        p.part[(int64_t)tj * p.job.I + i] = a;
+    }
 }
 
 // Joins a piece's statistics with those of the pieces before (run), and after the last
-// piece writes loss and lse.  A block takes RB rows, 1024 / RB threads per row walk the
-// entries, then a fixed tree joins them.
+// piece writes loss and lse, and the block's sum and count of losses.  A block of 1024
+// takes rb rows; 1024 / rb threads per row walk the tiles, a fixed tree joins them.  Few
+// rows go to one block, which then writes the mean too; otherwise rb is small enough for
+// many blocks (one block for 32 rows of 2048 entries took 27 us).
+struct Sum {
+    double loss;
+    int64_t n;
+};
 struct JoinParams {
-    const float2 *part;
-    float2 *run;
+    const pair_t *part;
+    pair_t *run;
     const float *zt;
     const int64_t *target;
     float *loss, *lse;
-    float *out; // mean written here when one block holds every row, or null
+    Sum *sum;   // [blocks]
+    float *out; // mean written here by the only block, or null
     int64_t M, V, parts;
     int first, last, rb;
 };
 
-__device__ __forceinline__ float2 join(float2 a, float2 b) {
-    const float m = fmaxf(a.x, b.x);
-    const float r = m == -INFINITY ? 0.0f : m; // nothing yet on either side
-    return make_float2(m, a.y * exp2_fast(a.x - r) + b.y * exp2_fast(b.x - r));
+__device__ __forceinline__ void write_mean(Sum s, float *out) {
+    const double inv = s.n ? 1.0 / (double)s.n : 0.0;
+    out[0] = s.n ? (float)(s.loss * inv) : 0.0f;
+    out[1] = (float)inv;
 }
-
-// mean of the counted losses and 1 / their number (0 of none) by one block of 1024
-__device__ __forceinline__ void mean_of(const float *loss, const int64_t *target, int64_t M, float *out, double *sd,
-                                        int64_t *sn) {
-    double d = 0.0;
-    int64_t n = 0;
-    for (int64_t i = threadIdx.x; i < M; i += 1024)
-        if (target[i] >= 0) {
-            d += (double)loss[i];
-            ++n;
-        }
-    sd[threadIdx.x] = d;
-    sn[threadIdx.x] = n;
-    __syncthreads();
-    for (int h = 512; h > 0; h >>= 1) {
-        if ((int)threadIdx.x < h) {
-            sd[threadIdx.x] += sd[threadIdx.x + h];
-            sn[threadIdx.x] += sn[threadIdx.x + h];
-        }
-        __syncthreads();
+__device__ __forceinline__ Sum wave_sum(Sum s) {
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1) {
+        s.loss += __shfl_xor(s.loss, h, 64);
+        s.n += __shfl_xor(s.n, h, 64);
     }
-    if (threadIdx.x == 0) {
-        const double inv = sn[0] ? 1.0 / (double)sn[0] : 0.0;
-        out[0] = sn[0] ? (float)(sd[0] * inv) : 0.0f;
-        out[1] = (float)inv;
-    }
+    return s;
 }
 
 __global__ __launch_bounds__(1024) void k_xent_join(JoinParams p) {
-    __shared__ float2 sh[1024];
-    __shared__ double sd[1024];
-    __shared__ int64_t sn[1024];
+    __shared__ pair_t sh[1024];
     const int rb = p.rb, per = 1024 / rb;
     const int r = threadIdx.x % rb, k = threadIdx.x / rb;
     const int64_t i = (int64_t)blockIdx.x * rb + r;
-    float2 a = make_float2(-INFINITY, 0.0f);
+    pair_t a = pair_t{-INFINITY, 0.0f};
     if (i < p.M) {
         if (k == 0 && !p.first)
             a = p.run[i];
-        for (int64_t e = k; e < p.parts; e += per)
-            a = join(a, p.part[e * p.M + i]);
+        for (int64_t e = k; e < p.parts; e += 4 * per) {
+            pair_t q[4]; // four loads in flight
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                q[u] = e + u * per < p.parts ? p.part[(e + u * per) * p.M + i] : pair_t{-INFINITY, 0.0f};
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                a = join(a, q[u]);
+        }
     }
     sh[threadIdx.x] = a;
     __syncthreads();
@@ -229,26 +250,51 @@ __global__ __launch_bounds__(1024) void k_xent_join(JoinParams p) {
             sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + h * rb]);
         __syncthreads();
     }
+    if (threadIdx.x >= 64) // rb <= 64: the rows' results are the first wave's
+        return;
+    Sum s{0.0, 0};
     if (k == 0 && i < p.M) {
         a = sh[r];
         p.run[i] = a;
         if (p.last) {
             const int64_t t = p.target[i];
             const float lse = (a.x + __builtin_log2f(a.y)) * kLn2;
+            const float loss = t < 0 ? 0.0f : t < p.V ? lse - p.zt[i] : NAN;
             p.lse[i] = t < 0 ? 0.0f : lse;
-            p.loss[i] = t < 0 ? 0.0f : t < p.V ? lse - p.zt[i] : NAN;
+            p.loss[i] = loss;
+            s = Sum{(double)loss, t >= 0};
         }
     }
-    if (p.last && p.out) {
-        __syncthreads(); // one block: its losses are visible to it
-        mean_of(p.loss, p.target, p.M, p.out, sd, sn);
+    if (p.last) {
+        s = wave_sum(s);
+        if (threadIdx.x == 0) {
+            if (p.out)
+                write_mean(s, p.out);
+            else
+                p.sum[blockIdx.x] = s;
+        }
     }
 }
 
-__global__ __launch_bounds__(1024) void k_xent_mean(const float *loss, const int64_t *target, int64_t M, float *out) {
-    __shared__ double sd[1024];
-    __shared__ int64_t sn[1024];
-    mean_of(loss, target, M, out, sd, sn);
+// mean of the counted losses and 1 / their number (0 of none), from the blocks' sums
+__global__ __launch_bounds__(256) void k_xent_mean(const Sum *sum, int64_t n, float *out) {
+    __shared__ Sum sh[4];
+    Sum s{0.0, 0};
+    for (int64_t i = threadIdx.x; i < n; i += 256) {
+        s.loss += sum[i].loss;
+        s.n += sum[i].n;
+    }
+    s = wave_sum(s);
+    if ((threadIdx.x & 63) == 0)
+        sh[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < 4; ++w) {
+            s.loss += sh[w].loss;
+            s.n += sh[w].n;
+        }
+        write_mean(s, out);
+    }
 }
 
 template <class T, int ROWS>
@@ -256,7 +302,7 @@ struct FwdCfg;
 template <class T> struct FwdCfg<T, xent::ROWS32> { using C = Cfg<T, 1, 4, 2, 2, false, true, 4>; };
 template <class T> struct FwdCfg<T, xent::ROWS64> { using C = Cfg<T, 1, 4, 4, 2, false, true, 3>; };
 template <class T> struct FwdCfg<T, xent::ROWS128> { using C = Cfg<T, 2, 2, 4, 4, false, true, 2>; };
-template <class T> struct FwdCfg<T, xent::ROWS256> { using C = Cfg<T, 2, 2, 8, 8, false, true, 2>; };
+template <class T> struct FwdCfg<T, xent::ROWS256> { using C = Cfg<T, 2, 2, 8, 8, false, true, 2, 3>; };
 
 template <class C>
 void set_tiles(Job &j) {
@@ -284,31 +330,40 @@ void stats(int rows, StatsParams &p, hipStream_t s) {
 bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // ---- backward --------------------------------------------------------------------------
-// Row parameters (one block).  fp16: the power of two that brings max |s| to
-// [2^14, 2^15); bf16 has fp32's range and takes 1.  scale[0], scale[1]: it and its inverse.
-struct RowsParams {
+// Row parameters, by the first block, and X's copy (rows that take no part as zeros: theirs
+// may hold anything), by the others.  fp16: the power of two that brings max |s| to
+// [2^14, 2^15); bf16 has fp32's range and takes 1.  pow2[0], pow2[1]: it and its inverse.
+struct PrepParams {
     const int64_t *target;
     const float *lse, *row_scale, *d_scale;
     float scale;
-    int64_t M, V;
+    int64_t M, K, V, Kp;
     int f16;
     RowParam *row;
     float *pow2;
+    const uint16_t *X;
+    uint16_t *x;
 };
 
-__global__ __launch_bounds__(1024) void k_xent_rows(RowsParams p) {
-    __shared__ float sh[1024];
+__global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
+    __shared__ float sh[256];
     const float base = p.scale * (p.d_scale ? p.d_scale[0] : 1.0f);
     auto s_of = [&](int64_t i) { return p.row_scale ? base * p.row_scale[i] : base; };
+    if (blockIdx.x > 0) {
+        pack_rows(p.X, p.K, p.M, p.K, p.x, p.Kp, (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x,
+                  (int64_t)(gridDim.x - 1) * 256, [&](int64_t r) { return p.target[r] >= 0 && s_of(r) != 0.0f; });
+        return;
+    }
     float f = 1.0f;
     if (p.f16) {
         float mx = 0.0f;
-        for (int64_t i = threadIdx.x; i < p.M; i += 1024)
+#pragma unroll 4
+        for (int64_t i = threadIdx.x; i < p.M; i += 256)
             if (p.target[i] >= 0)
                 mx = fmaxf(mx, fabsf(s_of(i)));
         sh[threadIdx.x] = mx;
         __syncthreads();
-        for (int h = 512; h > 0; h >>= 1) {
+        for (int h = 128; h > 0; h >>= 1) {
             if ((int)threadIdx.x < h)
                 sh[threadIdx.x] = fmaxf(sh[threadIdx.x], sh[threadIdx.x + h]);
             __syncthreads();
@@ -324,7 +379,8 @@ __global__ __launch_bounds__(1024) void k_xent_rows(RowsParams p) {
         p.pow2[0] = f;
         p.pow2[1] = 1.0f / f;
     }
-    for (int64_t i = threadIdx.x; i < p.M; i += 1024) {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < p.M; i += 256) {
         const int64_t t = p.target[i];
         const float s = s_of(i);
         RowParam r{0.0f, 0.0f, -1, 0}; // takes no part
@@ -333,58 +389,6 @@ __global__ __launch_bounds__(1024) void k_xent_rows(RowsParams p) {
         else if (t >= 0 && s != 0.0f)
             r = RowParam{p.lse[i] * kLog2e, s * f, (int)t, 0};
         p.row[i] = r;
-    }
-}
-
-// 16-bit output through LDS: 32 rows of a wave at a time, whole 16-byte chunks per lane.
-// value(x, y) gives the 4 packed values of acc[x][y].  VEC: rows of dst 16-byte aligned.
-template <class C, class Fn>
-__device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, int64_t I, int64_t J, int64_t ib, int64_t jb,
-                                        bool vec, LB_LDS char *smem, Fn value) {
-    constexpr int FJ = C::FJ, kRowB = FJ * 32, kChunks = 2 * FJ, kRows = 64 / kChunks;
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    LB_LDS char *const reg = smem + w * (FJ * 1024);
-#pragma unroll
-    for (int h = 0; h < C::FI / 2; ++h) {
-        pin(acc[2 * h]);
-        pin(acc[2 * h + 1]);
-#pragma unroll
-        for (int xx = 0; xx < 2; ++xx)
-#pragma unroll
-            for (int y = 0; y < FJ; ++y) {
-                const int r = 16 * xx + (lane & 15);
-                const int c = 2 * y + (lane >> 5); // 16-byte chunk: 8 columns
-                *reinterpret_cast<LB_LDS u32x2_t *>(reg + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4) +
-                                                    ((lane >> 4) & 1) * 8) = value(2 * h + xx, y);
-            }
-        const int64_t i0 = ib + 32 * h;
-        if (vec) {
-            u32x4_t v[FJ];
-#pragma unroll
-            for (int q = 0; q < FJ; ++q) {
-                const int r = q * kRows + lane / kChunks, c = lane % kChunks;
-                v[q] = *reinterpret_cast<const LB_LDS u32x4_t *>(reg + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4));
-            }
-            __builtin_amdgcn_sched_barrier(0); // all reads before the first store
-            const int64_t j = jb + 8 * (lane % kChunks);
-#pragma unroll
-            for (int q = 0; q < FJ; ++q) {
-                const int64_t i = i0 + q * kRows + lane / kChunks;
-                if (i < I && j < J)
-                    __builtin_nontemporal_store(v[q], reinterpret_cast<u32x4_t *>(dst + i * ld + j));
-            }
-        } else {
-            // rows of any alignment: 64 lanes store 64 neighbouring elements
-            for (int q = 0; q < 32 * FJ * 16 / 64; ++q) {
-                const int e = q * 64 + lane;
-                const int r = e / (FJ * 16), c = e % (FJ * 16);
-                const uint16_t v = *reinterpret_cast<const LB_LDS uint16_t *>(
-                    reg + r * kRowB + (((c >> 3) ^ (r & (kChunks - 1))) << 4) + (c & 7) * 2);
-                if (i0 + r < I && jb + c < J)
-                    dst[(i0 + r) * ld + jb + c] = v;
-            }
-        }
     }
 }
 
@@ -415,7 +419,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(Gr
         rp[x] = i < p.job.I ? p.row[i] : RowParam{0.0f, 0.0f, -1, 0};
     }
     const int j0 = (int)jb + 4 * (lane >> 4);
-    store16<C>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, smem, [&](int x, int y) {
+    store16<C>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, smem, [](int) {}, [&](int x, int y) {
         const int t = rp[x].t < 0 ? -1 : rp[x].t - (int)p.v0;
         float g[4];
 #pragma unroll
@@ -466,7 +470,7 @@ __device__ __forceinline__ void dx_tile(const BothParams &p, int b, LB_LDS char 
     float *const part = p.acc ? p.acc + (int64_t)sp * M * p.Kp : nullptr;
     const float f = p.pow2[1];
     const bool out = p.splits == 1 && p.last;
-    staged<C>(acc, i0, j0, smem, [&](int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
+    staged<C>(acc, i0, j0, smem, [](int, int64_t, int, int64_t) {}, [&](int, int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
         if (!p.first) {
             f32x4_t old[C::FJ];
 #pragma unroll
@@ -508,7 +512,7 @@ __device__ __forceinline__ void dw_tile(const BothParams &p, int b, LB_LDS char 
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
     const float f = p.pow2[1];
-    store16<C>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, smem, [&](int x, int y) {
+    store16<C>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, smem, [](int) {}, [&](int x, int y) {
         const f32x4_t &a = acc[x][y];
         return u32x2_t{C::T::pack2(a[0] * f, a[1] * f), C::T::pack2(a[2] * f, a[3] * f)};
     });
@@ -526,26 +530,39 @@ __global__ __launch_bounds__(kThreads, CX::TI == 256 ? 1 : 2) void k_xent_both(B
         dw_tile<CW>(p, p.dx_first ? b - lead : b, smem);
 }
 
-// dX from the ranges' partial sums, in range order
+// dX from the ranges' partial sums: 64 groups of four columns per block, each wave a
+// quarter of the ranges (in turn), the four sums added in wave order.
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_dx_sum(const float *acc, int splits, int64_t M, int64_t K, int64_t Kp,
                                                      const float *pow2, uint16_t *dX, int vec) {
+    __shared__ f32x4_t sh[4][64];
+    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
     const float f = pow2[1];
     const int64_t n = M * Kp / 4;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (int64_t)gridDim.x * 256) {
-        f32x4_t v = *reinterpret_cast<const f32x4_t *>(acc + 4 * q);
-        for (int s = 1; s < splits; ++s)
-            v += *reinterpret_cast<const f32x4_t *>(acc + (int64_t)s * M * Kp + 4 * q);
-        const int64_t r = 4 * q / Kp, c = 4 * q - r * Kp;
-        if (vec && c < K) {
-            *reinterpret_cast<u32x2_t *>(dX + r * K + c) =
-                u32x2_t{T::pack2(v[0] * f, v[1] * f), T::pack2(v[2] * f, v[3] * f)};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < K)
-                    dX[r * K + c + e] = T::one(v[e] * f);
+    for (int64_t q0 = (int64_t)blockIdx.x * 64; q0 < n; q0 += (int64_t)gridDim.x * 64) {
+        const int64_t q = q0 + lane;
+        f32x4_t v = {};
+        if (q < n) {
+#pragma unroll 4
+            for (int s = w; s < splits; s += 4)
+                v += *reinterpret_cast<const f32x4_t *>(acc + (int64_t)s * M * Kp + 4 * q);
         }
+        sh[w][lane] = v;
+        __syncthreads();
+        if (w == 0 && q < n) {
+            v = ((v + sh[1][lane]) + sh[2][lane]) + sh[3][lane];
+            const int64_t r = 4 * q / Kp, c = 4 * q - r * Kp;
+            if (vec && c < K) {
+                *reinterpret_cast<u32x2_t *>(dX + r * K + c) =
+                    u32x2_t{T::pack2(v[0] * f, v[1] * f), T::pack2(v[2] * f, v[3] * f)};
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + e < K)
+                        dX[r * K + c + e] = T::one(v[e] * f);
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -564,8 +581,8 @@ template <class T> struct BwdCfg<T, xent::ROWS128> {
     using W = Cfg<T, 2, 2, 4, 4, true, true, 2>;
 };
 template <class T> struct BwdCfg<T, xent::ROWS256> {
-    using X = Cfg<T, 2, 2, 8, 8, false, false, 2>;
-    using W = Cfg<T, 2, 2, 8, 8, true, true, 2>;
+    using X = Cfg<T, 2, 2, 8, 8, false, false, 2, 3>;
+    using W = Cfg<T, 2, 2, 8, 8, true, true, 2, 3>;
 };
 
 template <class T, int ROWS>
@@ -594,16 +611,17 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
     float *const pow2 = reinterpret_cast<float *>(ws + b.off_row + 16 * a.M);
     uint16_t *const x = reinterpret_cast<uint16_t *>(ws + b.off_x);
     uint16_t *const wp = reinterpret_cast<uint16_t *>(ws + b.off_w);
-    RowsParams rows{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.V, a.f16, row, pow2};
-    hipLaunchKernelGGL(k_xent_rows, dim3(1), dim3(1024), 0, s, rows);
-    pack(a.X, a.K, a.M, a.K, x, b.Kp, row, s);
+    PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16, row, pow2,
+                  static_cast<const uint16_t *>(a.X), x};
+    const int64_t copies = std::min<int64_t>(cdiv(a.M * (b.Kp / 8), 256), 8 * xent::kCUs);
+    hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(1 + copies)), dim3(256), 0, s, pp);
     const bool dx_vec = a.K % 4 == 0 && aligned(a.dX, 8);
     for (int64_t v0 = 0; v0 < a.V; v0 += b.Vc) {
         const int64_t vc = std::min(b.Vc, a.V - v0);
         const uint16_t *w = static_cast<const uint16_t *>(a.W) + v0;
         int64_t ldw = a.V;
         if (pack_w) {
-            pack(w, a.V, a.K, vc, wp, b.Vc, nullptr, s);
+            pack(w, a.V, a.K, vc, wp, b.Vc, s);
             w = wp;
             ldw = b.Vc;
         }
@@ -654,7 +672,7 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
         }
     }
     if (a.dX && b.splits > 1) {
-        const int64_t blocks = std::min<int64_t>(cdiv(a.M * b.Kp / 4, 256), 8 * xent::kCUs);
+        const int64_t blocks = std::min<int64_t>(cdiv(a.M * b.Kp / 4, 64), 32 * xent::kCUs);
         hipLaunchKernelGGL((k_xent_dx_sum<T>), dim3((unsigned)blocks), dim3(256), 0, s,
                            reinterpret_cast<const float *>(ws + b.off_acc), b.splits, a.M, a.K, b.Kp, pow2,
                            static_cast<uint16_t *>(a.dX), (int)dx_vec);
@@ -672,36 +690,35 @@ hipError_t forward(const XentArgs &a, hipStream_t s) {
     p.job.lda = a.K;
     if (a.K % 8 != 0 || !aligned(a.X, 16)) {
         uint16_t *const x = reinterpret_cast<uint16_t *>(ws + f.off_x);
-        pack(a.X, a.K, a.M, a.K, x, f.Kp, nullptr, s);
+        pack(a.X, a.K, a.M, a.K, x, f.Kp, s);
         p.job.a = x;
         p.job.lda = f.Kp;
     }
     p.job.I = a.M;
     p.job.R = a.K;
     p.target = a.target;
-    p.part = reinterpret_cast<float2 *>(ws + f.off_part);
+    p.part = reinterpret_cast<pair_t *>(ws + f.off_part);
     p.zt = reinterpret_cast<float *>(ws + f.off_zt);
     JoinParams j{};
     j.part = p.part;
-    j.run = reinterpret_cast<float2 *>(ws + f.off_run);
+    j.run = reinterpret_cast<pair_t *>(ws + f.off_run);
     j.zt = p.zt;
     j.target = a.target;
     j.loss = a.loss;
     j.lse = a.lse;
     j.M = a.M;
     j.V = a.V;
-    j.rb = 64;
-    while (j.rb > 1 && j.rb / 2 >= a.M)
-        j.rb /= 2;
-    const bool one = a.M <= j.rb; // one block joins every row and can write the mean
-    j.out = one ? a.out : nullptr;
+    j.sum = reinterpret_cast<Sum *>(ws + f.off_sum);
+    j.rb = f.join_rows;
+    const int64_t blocks = cdiv(a.M, j.rb);
+    j.out = blocks == 1 ? a.out : nullptr;
     for (int64_t v0 = 0; v0 < a.V; v0 += f.Vc) {
         const int64_t vc = std::min(f.Vc, a.V - v0);
         const uint16_t *w = static_cast<const uint16_t *>(a.W) + v0;
         p.job.ldb = a.V;
         if (pack_w) {
             uint16_t *const wp = reinterpret_cast<uint16_t *>(ws + f.off_w);
-            pack(w, a.V, a.K, vc, wp, f.Vc, nullptr, s);
+            pack(w, a.V, a.K, vc, wp, f.Vc, s);
             w = wp;
             p.job.ldb = f.Vc;
         }
@@ -709,13 +726,13 @@ hipError_t forward(const XentArgs &a, hipStream_t s) {
         p.job.J = vc;
         p.v0 = v0;
         stats<T>(f.rows, p, s);
-        j.parts = xent::up(vc, xent::tile_cols(f.rows)) / f.wcols;
+        j.parts = cdiv(vc, xent::tile_cols(f.rows));
         j.first = v0 == 0;
         j.last = v0 + f.Vc >= a.V;
-        hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv(a.M, j.rb)), dim3(1024), 0, s, j);
+        hipLaunchKernelGGL(k_xent_join, dim3((unsigned)blocks), dim3(1024), 0, s, j);
     }
-    if (!one)
-        hipLaunchKernelGGL(k_xent_mean, dim3(1), dim3(1024), 0, s, a.loss, a.target, a.M, a.out);
+    if (blocks > 1)
+        hipLaunchKernelGGL(k_xent_mean, dim3(1), dim3(256), 0, s, j.sum, blocks, a.out);
     return hipGetLastError();
 }
 
@@ -729,7 +746,7 @@ __global__ __launch_bounds__(256) void k_xent_zero(uint16_t *p, int64_t n) {
 
 hipError_t launch_lin_xent(const XentArgs &a, hipStream_t s) {
     if (a.M == 0) { // nothing counted: mean 0
-        hipLaunchKernelGGL(k_xent_mean, dim3(1), dim3(1024), 0, s, a.loss, a.target, (int64_t)0, a.out);
+        hipLaunchKernelGGL(k_xent_mean, dim3(1), dim3(256), 0, s, (const Sum *)nullptr, (int64_t)0, a.out);
         return hipGetLastError();
     }
     return a.f16 ? forward<F16>(a, s) : forward<BF16>(a, s);
