@@ -382,15 +382,102 @@ void launch(ProductParams &p, int64_t batch, hipStream_t s) {
 template <bool AOC, bool BOC, int STEP, bool FLAG>
 void product(ProductParams &p, int64_t batch, hipStream_t s) {
     const bool sym = (STEP == GRAM || STEP == ADD) && FLAG;
-    switch (muon::choose(batch, p.job.I, p.job.J, sym)) {
+    switch (muon::choose(batch, p.job.I, p.job.J, p.job.R, sym)) {
     case muon::TILE256: launch<Cfg<F16, 2, 2, 8, 8, AOC, BOC, 2, 3>, STEP, FLAG>(p, batch, s); break;
     case muon::TILE128: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 2>, STEP, FLAG>(p, batch, s); break;
-    default: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
+    case muon::TILE128_DEEP: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
+    default: launch<Cfg<F16, 2, 2, 2, 2, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
     }
 }
+// A and B = bA + cA² of a matrix whose shorter side fits one tile: the block writes A, in
+// fp16, to LDS as RC pairs (the ring is free by then), multiplies it by itself from there
+// and adds bA from its own registers.  Neither A nor a second launch touches memory.
+template <class C>
+__global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_poly(ProductParams p, float f2) {
+    static_assert(C::TI == C::TJ && C::FI == C::FJ && C::WI == 2, "one square tile");
+    if (p.skip && *p.skip)
+        return;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
+    LB_LDS char *smem = (LB_LDS char *)smem_raw;
+    constexpr int T = C::TI, F = C::FI;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Job job = p.job;
+    job.a += blockIdx.x * p.step_a;
+    job.b += blockIdx.x * p.step_b;
+    Acc<C> acc;
+    accumulate<C>(job, 0, 0, smem, acc);
+    // A as T/64 pairs of T rows of 128 bytes, chunk c of row o at c ^ (o % 8)
+    u32x2_t a[F][F];
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+        pin(acc[x]);
+#pragma unroll
+        for (int y = 0; y < F; ++y) {
+            const int i = (w / 2) * F * 16 + 16 * x + (lane & 15), j = (w % 2) * F * 16 + 16 * y + 4 * (lane >> 4);
+            const f32x4_t &t = acc[x][y];
+            a[x][y] = u32x2_t{F16::pack2(p.f * t[0], p.f * t[1]), F16::pack2(p.f * t[2], p.f * t[3])};
+            *reinterpret_cast<LB_LDS u32x2_t *>(smem + (j >> 6) * (T * 128) + i * 128 +
+                                                ((((j & 63) >> 3) ^ (i & 7)) << 4) + (j & 4) * 2) = a[x][y];
+            acc[x][y] = f32x4_t{};
+        }
+    }
+    __syncthreads();
+    Frags<T, false, F, 2> fa, fb;
+    fa.init(smem, (w / 2) * F * 16, lane);
+    fb.init(smem, (w % 2) * F * 16, lane);
+    frag_half_t unused[F][2];
+#pragma unroll
+    for (int h = 0; h < T / 32; ++h) {
+        u32x4_t af[F], bf[F];
+#pragma unroll
+        for (int k = 0; k < F; ++k) {
+            if (h & 1) {
+                fa.template read<0, 1>(k, (h >> 1) * (T * 128), af, unused);
+                fb.template read<0, 1>(k, (h >> 1) * (T * 128), bf, unused);
+            } else {
+                fa.template read<0, 0>(k, (h >> 1) * (T * 128), af, unused);
+                fb.template read<0, 0>(k, (h >> 1) * (T * 128), bf, unused);
+            }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        Frags<T, false, F, 2>::settle(af, unused);
+        Frags<T, false, F, 2>::settle(bf, unused);
+#pragma unroll
+        for (int x = 0; x < F; ++x)
+#pragma unroll
+            for (int y = 0; y < F; ++y)
+                F16::mfma(acc[x][y], bf[y], af[x]);
+    }
+    mfma_drain();
+    __syncthreads(); // every wave has read A: the epilogue may stage over it
+    store16<C>(
+        acc, p.out + blockIdx.x * p.step_out, p.ld_out, job.I, (job.J + 7) / 8 * 8, (w / 2) * F * 16, (w % 2) * F * 16,
+        true, smem, [](int) {},
+        [&](int x, int y) {
+            const f32x4_t old = f16x4(a[x][y]);
+            f32x4_t t;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                t[e] = __builtin_fmaf(p.fa, old[e], f2 * acc[x][y][e]);
+            return u32x2_t{F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
+        });
+}
+
+template <bool OC>
+void one_tile_poly(int T, ProductParams &p, float f2, int64_t batch, hipStream_t s) {
+    p.job.tiles_i = p.job.tiles_j = p.job.group = 1;
+    if (T == 64)
+        hipLaunchKernelGGL((k_muon_poly<Cfg<F16, 2, 2, 2, 2, OC, OC, 4>>), dim3((unsigned)batch), dim3(kThreads), 0, s,
+                           p, f2);
+    else
+        hipLaunchKernelGGL((k_muon_poly<Cfg<F16, 2, 2, 4, 4, OC, OC, 4>>), dim3((unsigned)batch), dim3(kThreads), 0, s,
+                           p, f2);
+}
+
 template <bool AOC, bool BOC, int STEP>
 void symmetric_product(ProductParams &p, int64_t batch, hipStream_t s) {
-    if (muon::lower_only(batch, p.job.I))
+    if (muon::lower_only(batch, p.job.I, p.job.R))
         product<AOC, BOC, STEP, true>(p, batch, s);
     else
         product<AOC, BOC, STEP, false>(p, batch, s);
@@ -471,13 +558,20 @@ hipError_t launch_muon(const MuonArgs &a, hipStream_t s) {
     upd.scale = a.scale;
     upd.wd = a.wd;
     upd.skip = a.skip;
+    const int one = muon::one_tile(a.batch, pl.s, gram.job.R);
     for (int t = 0; t < a.steps; ++t) {
         gram.job.a = gram.job.b = x;
-        if (pl.tall)
+        if (one) { // A stays in LDS, B comes out
+            gram.fa = kB;
+            gram.out = gb;
+            pl.tall ? one_tile_poly<true>(one, gram, poly.f, a.batch, s)
+                    : one_tile_poly<false>(one, gram, poly.f, a.batch, s);
+        } else if (pl.tall)
             symmetric_product<true, true, GRAM>(gram, a.batch, s);
         else
             symmetric_product<false, false, GRAM>(gram, a.batch, s);
-        symmetric_product<false, false, ADD>(poly, a.batch, s);
+        if (!one)
+            symmetric_product<false, false, ADD>(poly, a.batch, s);
         const bool last = t + 1 == a.steps;
         upd.job.a = pl.tall ? x : gb;
         upd.job.b = pl.tall ? gb : x;

@@ -14,11 +14,37 @@ constexpr int64_t kMaxWidth = (int64_t)1 << 22; // K and V stay below: 256 rows 
 inline int64_t up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline int64_t cdiv(int64_t x, int64_t m) { return (x + m - 1) / m; }
 
-// Row tiles: 32, 64 or 128 rows (x 128 columns) for small M, 256 x 256 otherwise.
-enum Rows { ROWS32 = 0, ROWS64 = 1, ROWS128 = 2, ROWS256 = 3 };
-inline int tile_rows(int r) { return 32 << r; }
-inline int tile_cols(int r) { return r == ROWS256 ? 256 : 128; }
-inline int choose_rows(int64_t M) { return M <= 32 ? ROWS32 : M <= 64 ? ROWS64 : M <= 128 ? ROWS128 : ROWS256; }
+// Tile shapes.  Microseconds of a tile over p pairs of slabs (64 reduction indices each),
+// measured on the card with single products from 64 x 64 to 4096 x 12288: fixed + p * alone
+// with a CU to itself, fixed + p * full with `slots` of them on the card.
+struct Shape {
+    int ti, tj, slots;
+    double fixed, alone, full;
+};
+enum Rows { ROWS32 = 0, ROWS64 = 1, ROWS128 = 2, ROWS256 = 3, SQUARE64 = 4 };
+inline Shape shape(int r) {
+    switch (r) {
+    case ROWS32: return {32, 128, 2 * kCUs, 2.9, 0.25, 0.45};
+    case ROWS64: return {64, 128, 2 * kCUs, 3.1, 0.30, 0.57};
+    case ROWS128: return {128, 128, 2 * kCUs, 3.8, 0.36, 0.65};
+    case ROWS256: return {256, 256, kCUs, 11.0, 1.03, 1.03};
+    default: return {64, 64, 2 * kCUs, 2.8, 0.24, 0.34};
+    }
+}
+inline int64_t tiles(int r, int64_t I, int64_t J) { return cdiv(I, shape(r).ti) * cdiv(J, shape(r).tj); }
+// a launch of n equal tiles
+inline double launch_us(int r, int64_t n, int64_t p) {
+    const Shape s = shape(r);
+    return n <= kCUs ? s.fixed + s.alone * p : cdiv(n, s.slots) * (s.fixed + s.full * p);
+}
+// The logits' tiles: X's rows by the vocabulary's columns, over K.
+inline int choose_rows(int64_t M, int64_t K, int64_t V) {
+    int best = ROWS32;
+    for (int r : {ROWS64, ROWS128, ROWS256})
+        if (launch_us(r, tiles(r, M, V), cdiv(K, 64)) < launch_us(best, tiles(best, M, V), cdiv(K, 64)))
+            best = r;
+    return best;
+}
 
 // A packed copy of W's piece (V not a multiple of 8, or W not 16-byte aligned) takes at
 // most this.  Large pieces waste fewer part-filled rounds of tiles (pieces of 128 MiB,
@@ -49,9 +75,9 @@ struct Fwd {
 
 inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     Fwd f;
-    f.rows = choose_rows(M);
+    f.rows = choose_rows(M, K, V);
     f.Kp = up(K, 8);
-    const int64_t cols = tile_cols(f.rows);
+    const int64_t cols = shape(f.rows).tj;
     f.Vc = piece(V, cdiv(8 * M, cols), kPartBytes);
     if (pack_w)
         f.Vc = std::min(f.Vc, piece(V, 2 * K, kPackBytes));
@@ -76,8 +102,25 @@ inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     return f;
 }
 
+// The tiles of dX (rows of X by K, over a piece of Vc columns, in ranges) and dW (K by Vc,
+// over the rows) share a launch.
+struct Pair {
+    int x, w; // Rows
+};
+enum Both { X32_W128 = 0, X64_W128 = 1, X128_W128 = 2, X256_W256 = 3, X64_W64 = 4 };
+inline Pair pair(int both) {
+    switch (both) {
+    case X32_W128: return {ROWS32, ROWS128};
+    case X64_W128: return {ROWS64, ROWS128};
+    case X128_W128: return {ROWS128, ROWS128};
+    case X256_W256: return {ROWS256, ROWS256};
+    default: return {SQUARE64, SQUARE64};
+    }
+}
+
 struct Bwd {
-    int rows;
+    int rows;          // Rows of the logits' tiles
+    int both;          // Both
     int64_t Kp, Vc;
     int splits;        // dX's reduction over a piece, in this many ranges
     int64_t split_len; // a multiple of 64
@@ -85,32 +128,50 @@ struct Bwd {
     int64_t off_row, off_x, off_w, off_g, off_acc, bytes;
 };
 
-// dX over a piece of Vc columns beside dW over M rows.  A dX tile walks Vc columns, a dW
-// tile M rows; where M is small one dX tile would outlast everything else, so its
-// reduction is split until a tile is at most half of what a CU gets on average (or
-// 1024 columns), within the partial sums' room.
-inline int dx_splits(int64_t M, int64_t Kp, int64_t Vc, int rows) {
-    const int tr = tile_rows(rows), tc = tile_cols(rows);
-    const int dwr = rows == ROWS256 ? 256 : 128;
-    const int64_t slots = rows == ROWS256 ? kCUs : 2 * kCUs;
-    const int64_t ntx = cdiv(M, tr) * cdiv(Kp, tc);
-    const int64_t ntw = cdiv(Kp, dwr) * cdiv(Vc, dwr);
-    const int64_t total = ntx * cdiv(Vc, 64) + ntw * cdiv(M, 64);
-    const int64_t target = std::max<int64_t>(8, total / slots / 2); // pairs of slabs
-    int64_t s = cdiv(cdiv(Vc, 64), target);
+// A dX tile walks Vc columns, a dW tile M rows; where M is small one dX tile would outlast
+// everything else, so its reduction is split until a tile takes at most half of what a
+// slot gets on average (or 8 pairs of slabs), within the partial sums' room.
+inline int dx_splits(int64_t M, int64_t Kp, int64_t Vc, int both) {
+    const Pair c = pair(both);
+    const int64_t ntx = tiles(c.x, M, Kp), ntw = tiles(c.w, Kp, Vc);
+    const Shape x = shape(c.x), w = shape(c.w);
+    const int64_t px = cdiv(Vc, 64), pw = cdiv(M, 64);
+    const double per_slot = (ntx * (px * x.full) + ntw * (pw * w.full + w.fixed)) / x.slots;
+    const int64_t target = std::max<int64_t>(8, (int64_t)(per_slot / 2 / x.full));
+    int64_t s = cdiv(px, target);
     s = std::min<int64_t>(s, std::max<int64_t>(1, kSplitBytes / (4 * M * Kp)));
-    s = std::min<int64_t>(s, 64);
-    return (int)std::max<int64_t>(1, s);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(s, 64));
+}
+inline double both_us(int64_t M, int64_t Kp, int64_t Vc, int both) {
+    const Pair c = pair(both);
+    const int s = dx_splits(M, Kp, Vc, both);
+    const int64_t nx = tiles(c.x, M, Kp) * s, nw = tiles(c.w, Kp, Vc);
+    const Shape x = shape(c.x), w = shape(c.w);
+    const double px = (double)cdiv(cdiv(Vc, s), 64), pw = (double)cdiv(M, 64);
+    // partial sums written and read back at 5 TB/s
+    const double sums = s > 1 ? 3.5 + 8.0 * M * Kp * s / 5e6 : 0.0;
+    if (nx + nw <= kCUs)
+        return std::max(x.fixed + x.alone * px, w.fixed + w.alone * pw) + sums;
+    const double tx = x.fixed + x.full * px, tw = w.fixed + w.full * pw;
+    return (nx * tx + nw * tw) / x.slots + 0.5 * std::max(tx, tw) + sums;
+}
+inline int choose_both(int64_t M, int64_t Kp, int64_t Vc) {
+    int best = X32_W128;
+    for (int b : {X64_W128, X128_W128, X256_W256, X64_W64})
+        if (both_us(M, Kp, Vc, b) < both_us(M, Kp, Vc, best))
+            best = b;
+    return best;
 }
 
 inline Bwd backward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     Bwd b;
-    b.rows = choose_rows(M);
+    b.rows = choose_rows(M, K, V);
     b.Kp = up(K, 8);
     b.Vc = piece(V, 2 * M, kGradBytes);
     if (pack_w)
         b.Vc = std::min(b.Vc, piece(V, 2 * K, kPackBytes));
-    b.splits = dx_splits(M, b.Kp, b.Vc, b.rows);
+    b.both = choose_both(M, b.Kp, b.Vc);
+    b.splits = dx_splits(M, b.Kp, b.Vc, b.both);
     b.split_len = up(cdiv(b.Vc, b.splits), 64);
     b.splits = (int)cdiv(b.Vc, b.split_len);
     b.acc = b.splits > 1 || b.Vc < V;

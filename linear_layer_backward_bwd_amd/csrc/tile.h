@@ -16,9 +16,8 @@
 //
 //   RC  T rows of 128 B (whole cache lines); 16-byte chunk c of row o sits at
 //       chunk c ^ (o % 8); a 16x16x32 fragment is one ds_read_b128.
-//   OC  64 rows (r) of 2T bytes; chunk c of row r sits at
-//       c ^ 2*((r & 3) | 4*((r >> 3) & 1)); a fragment is two transposing reads
-//       (ds_read_b64_tr_b16), each a 4-row x 16-column block per 16 lanes.
+//   OC  64 rows (r) of 2T bytes; chunk c of row r sits at c ^ swz_oc(r); a fragment is two
+//       transposing reads (ds_read_b64_tr_b16), each a 4-row x 16-column block per 16 lanes.
 //
 // Both patterns read without bank conflicts (the layouts of the Linear backward's
 // tile kernel).  While the MFMAs of one slab run on fragments in registers, the
@@ -80,8 +79,8 @@ struct Cfg {
     static constexpr int kDma = kDmaA + kDmaB;
     static_assert(WI * WJ == 4, "four waves");
     static_assert(TI % 32 == 0 && TJ % 32 == 0, "whole DMA instructions per wave");
-    static_assert(!AOC || TI == 128 || TI == 256, "OC rows of 256 or 512 bytes");
-    static_assert(!BOC || TJ == 128 || TJ == 256, "OC rows of 256 or 512 bytes");
+    static_assert(!AOC || TI == 64 || TI == 128 || TI == 256, "OC rows of 128, 256 or 512 bytes");
+    static_assert(!BOC || TJ == 64 || TJ == 128 || TJ == 256, "OC rows of 128, 256 or 512 bytes");
     static_assert(4 * FJ * 1024 <= kLds, "the epilogue stages 16 rows per wave in the ring");
     // DMA instructions that may be in flight while the next pair has landed
     static constexpr int kAhead = (S - 2) * kDma + (SB - S) * kDmaB;
@@ -116,7 +115,16 @@ __device__ __forceinline__ void vm_wait() {
 // Publishes landed DMA and retires this wave's LDS reads; no fence, so DMA stays in flight.
 __device__ __forceinline__ void ring_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ __forceinline__ int swz_oc(int row) { return 2 * ((row & 3) | (((row >> 3) & 1) << 2)); }
+// XOR on an OC row's chunk index: the rows r..r+3 and r+8..r+11 of one 32-lane read land on
+// eight different 32-byte segments of the 256 bytes of banks (rows of 128 bytes alternate
+// between two halves by themselves, so four segments are left to choose).
+template <int T>
+__device__ __forceinline__ int swz_oc(int row) {
+    if constexpr (T >= 128)
+        return 2 * ((row & 3) | (((row >> 3) & 1) << 2));
+    else
+        return 2 * (((row >> 1) & 1) | (((row >> 3) & 1) << 1));
+}
 
 // Block index -> tile.  Blocks are dealt to the 8 XCDs in turn, so each XCD's blocks are
 // first gathered into one contiguous range (any count), then rastered in groups of
@@ -175,7 +183,7 @@ struct Side {
 #pragma unroll
             for (int d = 0; d < kDmaN; ++d) {
                 const int row = (w * kDmaN + d) * kRows + lane / kChunks;
-                const int c = (lane % kChunks) ^ swz_oc(row);
+                const int c = (lane % kChunks) ^ swz_oc<T>(row);
                 off[d] = (uint32_t)((row * ld + 8 * c) * 2) | ((uint32_t)!(8 * c < span) << 31);
             }
         } else {
@@ -231,7 +239,7 @@ struct Frags {
 #pragma unroll
             for (int x = 0; x < F; ++x) {
                 const int col = ob + 16 * x + 4 * (s & 3);
-                base[x] = region + row * (2 * T) + (((col >> 3) ^ swz_oc(row)) << 4) + (col & 7) * 2;
+                base[x] = region + row * (2 * T) + (((col >> 3) ^ swz_oc<T>(row)) << 4) + (col & 7) * 2;
             }
         } else {
 #pragma unroll

@@ -450,6 +450,7 @@ struct BothParams {
     int dw_tiles;      // blocks of dW; 0: not wanted
     int dx_tiles;      // blocks of dX
     int dx_first;      // the longer tiles are launched first
+    int want_dx;
 };
 
 template <class C>
@@ -566,40 +567,65 @@ __global__ __launch_bounds__(256) void k_xent_dx_sum(const float *acc, int split
     }
 }
 
-template <class T, int ROWS>
+template <class T, int BOTH>
 struct BwdCfg;
-template <class T> struct BwdCfg<T, xent::ROWS32> {
+template <class T> struct BwdCfg<T, xent::X32_W128> {
     using X = Cfg<T, 1, 4, 2, 2, false, false, 4>;
     using W = Cfg<T, 2, 2, 4, 4, true, true, 2>;
 };
-template <class T> struct BwdCfg<T, xent::ROWS64> {
+template <class T> struct BwdCfg<T, xent::X64_W128> {
     using X = Cfg<T, 1, 4, 4, 2, false, false, 3>;
     using W = Cfg<T, 2, 2, 4, 4, true, true, 2>;
 };
-template <class T> struct BwdCfg<T, xent::ROWS128> {
+template <class T> struct BwdCfg<T, xent::X128_W128> {
     using X = Cfg<T, 2, 2, 4, 4, false, false, 2>;
     using W = Cfg<T, 2, 2, 4, 4, true, true, 2>;
 };
-template <class T> struct BwdCfg<T, xent::ROWS256> {
+template <class T> struct BwdCfg<T, xent::X256_W256> {
     using X = Cfg<T, 2, 2, 8, 8, false, false, 2, 3>;
     using W = Cfg<T, 2, 2, 8, 8, true, true, 2, 3>;
 };
+template <class T> struct BwdCfg<T, xent::X64_W64> {
+    using X = Cfg<T, 2, 2, 2, 2, false, false, 4>;
+    using W = Cfg<T, 2, 2, 2, 2, true, true, 4>;
+};
 
-template <class T, int ROWS>
-void piece_bwd(GradParams &g, BothParams &p, bool want_dx, bool want_dw, hipStream_t s) {
-    using CG = typename FwdCfg<T, ROWS>::C;
-    using CX = typename BwdCfg<T, ROWS>::X;
-    using CW = typename BwdCfg<T, ROWS>::W;
-    set_tiles<CG>(g.job);
+template <class C>
+void run_grad(GradParams &g, hipStream_t s) {
+    set_tiles<C>(g.job);
     // G's padding columns (up to a multiple of 64) are zeroed by the tiles that own them
-    g.job.tiles_j = (int)cdiv(g.Vg, CG::TJ);
-    hipLaunchKernelGGL((k_xent_grad<CG>), dim3((unsigned)(g.job.tiles_i * g.job.tiles_j)), dim3(kThreads), 0, s, g);
+    g.job.tiles_j = (int)cdiv(g.Vg, C::TJ);
+    hipLaunchKernelGGL((k_xent_grad<C>), dim3((unsigned)(g.job.tiles_i * g.job.tiles_j)), dim3(kThreads), 0, s, g);
+}
+template <class T>
+void grad(int rows, GradParams &g, hipStream_t s) {
+    switch (rows) {
+    case xent::ROWS32: run_grad<typename FwdCfg<T, xent::ROWS32>::C>(g, s); break;
+    case xent::ROWS64: run_grad<typename FwdCfg<T, xent::ROWS64>::C>(g, s); break;
+    case xent::ROWS128: run_grad<typename FwdCfg<T, xent::ROWS128>::C>(g, s); break;
+    default: run_grad<typename FwdCfg<T, xent::ROWS256>::C>(g, s); break;
+    }
+}
+template <class T, int BOTH>
+void run_both(BothParams &p, hipStream_t s) {
+    using CX = typename BwdCfg<T, BOTH>::X;
+    using CW = typename BwdCfg<T, BOTH>::W;
     set_tiles<CX>(p.dx);
     set_tiles<CW>(p.dw);
-    p.dx_tiles = want_dx ? p.dx.tiles_i * p.dx.tiles_j * p.splits : 0;
-    p.dw_tiles = want_dw ? p.dw.tiles_i * p.dw.tiles_j : 0;
+    p.dx_tiles = p.want_dx ? p.dx.tiles_i * p.dx.tiles_j * p.splits : 0;
+    p.dw_tiles = p.dW ? p.dw.tiles_i * p.dw.tiles_j : 0;
     p.dx_first = p.split_len * CX::TI * CX::TJ >= p.dw.R * CW::TI * CW::TJ;
     hipLaunchKernelGGL((k_xent_both<CX, CW>), dim3((unsigned)(p.dx_tiles + p.dw_tiles)), dim3(kThreads), 0, s, p);
+}
+template <class T>
+void both(int which, BothParams &p, hipStream_t s) {
+    switch (which) {
+    case xent::X32_W128: run_both<T, xent::X32_W128>(p, s); break;
+    case xent::X64_W128: run_both<T, xent::X64_W128>(p, s); break;
+    case xent::X128_W128: run_both<T, xent::X128_W128>(p, s); break;
+    case xent::X256_W256: run_both<T, xent::X256_W256>(p, s); break;
+    default: run_both<T, xent::X64_W64>(p, s); break;
+    }
 }
 
 template <class T>
@@ -664,12 +690,9 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
         p.ldw = a.V;
         p.dw_vec = a.V % 8 == 0 && aligned(a.dW, 16);
         p.pow2 = pow2;
-        switch (b.rows) {
-        case xent::ROWS32: piece_bwd<T, xent::ROWS32>(g, p, a.dX, a.dW, s); break;
-        case xent::ROWS64: piece_bwd<T, xent::ROWS64>(g, p, a.dX, a.dW, s); break;
-        case xent::ROWS128: piece_bwd<T, xent::ROWS128>(g, p, a.dX, a.dW, s); break;
-        default: piece_bwd<T, xent::ROWS256>(g, p, a.dX, a.dW, s); break;
-        }
+        p.want_dx = a.dX != nullptr;
+        grad<T>(b.rows, g, s);
+        both<T>(b.both, p, s);
     }
     if (a.dX && b.splits > 1) {
         const int64_t blocks = std::min<int64_t>(cdiv(a.M * b.Kp / 4, 64), 32 * xent::kCUs);
@@ -726,7 +749,7 @@ hipError_t forward(const XentArgs &a, hipStream_t s) {
         p.job.J = vc;
         p.v0 = v0;
         stats<T>(f.rows, p, s);
-        j.parts = cdiv(vc, xent::tile_cols(f.rows));
+        j.parts = cdiv(vc, xent::shape(f.rows).tj);
         j.first = v0 == 0;
         j.last = v0 + f.Vc >= a.V;
         hipLaunchKernelGGL(k_xent_join, dim3((unsigned)blocks), dim3(1024), 0, s, j);
