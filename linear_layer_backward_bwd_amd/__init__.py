@@ -366,8 +366,9 @@ class _on_device:
 
     def __enter__(self):
         import torch
-        if torch.cuda.current_device() != self.dev.index:
-            self.back = torch.cuda.current_device()
+        now = torch.cuda.current_device()
+        if now != self.dev.index:
+            self.back = now
             torch.cuda.set_device(self.dev)
         _use_current_stream(self.dev)
 

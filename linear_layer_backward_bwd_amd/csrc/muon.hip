@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void k_muon_norm(PrepParams p) {
         p.part[(int64_t)blockIdx.y * p.parts + blockIdx.x] = sh[0];
 }
 
-// X = u / ‖u‖_F in fp16, rows padded with zeros to a multiple of 8.  ‖u‖ = 0 gives 0, a
+// X = u / ‖u‖_F in fp16, rows padded with zeros to a multiple of 64.  ‖u‖ = 0 gives 0, a
 // norm that is infinite or NaN gives NaN throughout.
 template <int GT, bool VEC>
 __global__ __launch_bounds__(256) void k_muon_scale(PrepParams p) {
@@ -140,35 +140,54 @@ __global__ __launch_bounds__(256) void k_muon_scale(PrepParams p) {
             sh[threadIdx.x] += sh[threadIdx.x + h];
         __syncthreads();
     }
+    // 2^15 / ‖u‖ as a float in [0.5, 1) and a power of two: no intermediate leaves fp32's range
     const double norm = sqrt(sh[0]);
-    const double f = norm == 0.0 ? 0.0 : norm < INFINITY ? (double)kX / norm : NAN;
+    int e = 0;
+    const float f = norm == 0.0 ? 0.0f : norm < INFINITY ? (float)frexp((double)kX / norm, &e) : NAN;
     const float clip = p.clip ? *p.clip : 1.0f;
     const int64_t base = (int64_t)blockIdx.y * p.K * p.N;
     uint16_t *const x = p.x + (int64_t)blockIdx.y * p.K * p.Np;
-    const int64_t per = p.Np / 4, n = p.K * per;
-    for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n; q += (int64_t)gridDim.x * 256) {
-        const int64_t r = q / per, c = (q - r * per) * 4, i = base + r * p.N + c;
-        f32x4_t g{}, m{};
-        if (VEC && c < p.N) {
-            g = grad4_at<GT>(p.g, i);
-            if (p.mom)
-                m = *reinterpret_cast<const f32x4_t *>(p.mom + i);
-        } else {
+    const int64_t per = p.Np / 8, first = (int64_t)blockIdx.x * 256 + threadIdx.x, stride = (int64_t)gridDim.x * 256;
+    const int64_t step_r = stride / per, step_q = stride - step_r * per;
+    int64_t r = first / per, q = first - r * per; // one division, then steps
+    for (; r < p.K; r += step_r, q += step_q) {
+        if (q >= per) {
+            q -= per;
+            if (++r >= p.K)
+                break;
+        }
+        const int64_t c = q * 8, i = base + r * p.N + c;
+        f32x4_t g[2] = {}, m[2] = {};
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < p.N) {
-                    g[e] = grad_at<GT>(p.g, i + e);
-                    m[e] = p.mom ? p.mom[i + e] : 0.0f;
+        for (int k = 0; k < 2; ++k) {
+            if (VEC) {
+                if (c + 4 * k < p.N) {
+                    g[k] = grad4_at<GT>(p.g, i + 4 * k);
+                    if (p.mom)
+                        m[k] = *reinterpret_cast<const f32x4_t *>(p.mom + i + 4 * k);
                 }
-        }
-        uint16_t h[4];
+            } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float u = update_of(unscaled(g[e], p.inv_scale, clip), m[e], p);
-            h[e] = c + e < p.N ? F16::one((float)((double)u * f)) : (uint16_t)0;
+                for (int d = 0; d < 4; ++d)
+                    if (c + 4 * k + d < p.N) {
+                        g[k][d] = grad_at<GT>(p.g, i + 4 * k + d);
+                        m[k][d] = p.mom ? p.mom[i + 4 * k + d] : 0.0f;
+                    }
+            }
         }
-        *reinterpret_cast<u32x2_t *>(x + r * p.Np + c) =
-            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
+        u32x4_t h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            float u[2];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int n = 2 * k + d;
+                const float v = update_of(unscaled(g[n >> 2][n & 3], p.inv_scale, clip), m[n >> 2][n & 3], p);
+                u[d] = c + n < p.N ? ldexpf(v, e) * f : 0.0f; // a padding column stays 0 whatever f is
+            }
+            h[k] = F16::pack2(u[0], u[1]);
+        }
+        *reinterpret_cast<u32x4_t *>(x + r * p.Np + c) = h;
     }
 }
 
@@ -182,11 +201,12 @@ enum Step {
 
 struct ProductParams {
     Job job;
+    int tiles;              // of one matrix
     int64_t step_a, step_b; // elements from one matrix to the next
     float f, fa;
     const uint16_t *add; // fp16
     int64_t ld_add, step_add;
-    uint16_t *out; // fp16, ld a multiple of 8
+    uint16_t *out; // fp16, ld a multiple of 64
     int64_t ld_out, step_out;
     // the caller's matrices, [batch][I][J]
     uint16_t *o;
@@ -201,39 +221,60 @@ __device__ __forceinline__ f32x4_t f16x4(const u32x2_t &h) {
     return f32x4_t{F16::f32(h[0]), F16::f32(h[0] >> 16), F16::f32(h[1]), F16::f32(h[1] >> 16)};
 }
 
+// A 4 x 4 block of 16-bit values held by four neighbouring lanes (lane q: row q) transposed:
+// lane q gets the values of column mirror_row(q).  Two exchanges within the quad.
+__device__ __forceinline__ int mirror_row(int lane) { return ((lane & 1) << 1) | ((lane >> 1) & 1); }
+__device__ __forceinline__ u32x2_t transposed4(const u32x2_t &h, int lane) {
+    const bool odd = lane & 1, upper = lane & 2;
+    const uint32_t own = odd ? h[1] : h[0];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)(odd ? h[0] : h[1]), 0xB1, 0xf, 0xf, true); // lane ^ 1
+    const uint32_t lo = odd ? got : own, hi = odd ? own : got;
+    const uint32_t d0 = (lo & 0xffffu) | (hi << 16), d1 = (lo >> 16) | (hi & 0xffff0000u);
+    const uint32_t far = (uint32_t)__builtin_amdgcn_mov_dpp((int)(upper ? d0 : d1), 0x4E, 0xf, 0xf, true); // lane ^ 2
+    return upper ? u32x2_t{far, d1} : u32x2_t{d0, far};
+}
+
 // GRAM and the ADD that makes B are symmetric (SYM): only the tiles on and below
 // the diagonal run, and each stores its mirror image too.  What is added is loaded one
 // round of the epilogue ahead (the first before the main loop): with the loads in the
 // round that uses them, A² at 4096 took 120 us.
 template <class C, int STEP, bool SYM>
-__device__ __forceinline__ void store_small(const ProductParams &p, const Job &job, int ti, int tj, LB_LDS char *smem) {
+__device__ __forceinline__ void store_small(const ProductParams &p, const Job &job, int64_t b, int ti, int tj,
+                                            LB_LDS char *smem) {
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t I = job.I, Jp = (job.J + 7) / 8 * 8;
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
-    const uint16_t *const add = p.add + blockIdx.y * p.step_add;
-    uint16_t *const out = p.out + blockIdx.y * p.step_out;
+    const uint16_t *const add = p.add + b * p.step_add;
+    uint16_t *const out = p.out + b * p.step_out;
     u32x2_t next[2][C::FJ], cur[2][C::FJ];
+    // rows past I read zero, columns past the padding are another row's and not stored
+    const uint32_t add_off = (uint32_t)((lane & 15) * p.ld_add + 4 * (lane >> 4)) * 2;
     auto load = [&](int h) {
         if constexpr (STEP == ADD) {
+            const int64_t i0 = ib + 32 * h, rows = max<int64_t>(0, min<int64_t>(32, I - i0));
+            const __amdgpu_buffer_rsrc_t rs =
+                rsrc(add + i0 * p.ld_add + jb, rows && jb < Jp ? (uint32_t)((rows * p.ld_add - jb) * 2) : 0u);
 #pragma unroll
-            for (int xx = 0; xx < 2; ++xx) {
-                const int64_t i = ib + 32 * h + 16 * xx + (lane & 15);
+            for (int xx = 0; xx < 2; ++xx)
 #pragma unroll
-                for (int y = 0; y < C::FJ; ++y) {
-                    const int64_t j = jb + 16 * y + 4 * (lane >> 4);
-                    next[xx][y] = i < I && j < Jp ? *reinterpret_cast<const u32x2_t *>(add + i * p.ld_add + j)
-                                                  : u32x2_t{};
-                }
-            }
+                for (int y = 0; y < C::FJ; ++y)
+                    next[xx][y] = __builtin_bit_cast(
+                        u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                     rs, (int)(add_off + 32 * xx * (uint32_t)p.ld_add + 32 * y), 0, 0));
         }
     };
     load(0);
     Acc<C> acc;
     accumulate<C>(job, ti, tj, smem, acc);
     const bool mirror = SYM && ti != tj;
-    store16<C>(
+    // the wave's mirror image: FJ*16 rows from row jb, from column ib on
+    const int64_t mrows = max<int64_t>(0, min<int64_t>(C::FJ * 16, I - jb));
+    const __amdgpu_buffer_rsrc_t mrs = rsrc(out + jb * p.ld_out + ib, (uint32_t)(mrows * p.ld_out * 2));
+    const uint32_t mirror_off =
+        (uint32_t)((4 * (lane >> 4) + mirror_row(lane)) * p.ld_out + (lane & 12)) * 2;
+    store16<C, false>(
         acc, out, p.ld_out, I, Jp, ib, jb, true, smem,
         [&](int h) {
 #pragma unroll
@@ -256,13 +297,11 @@ __device__ __forceinline__ void store_small(const ProductParams &p, const Job &j
                     t[e] = __builtin_fmaf(p.fa, a[e], t[e]);
             }
             const u32x2_t h = {F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
-            if (mirror) { // 16 lanes of one column: 32 bytes of a row of the mirror image
-                const int64_t i = ib + 16 * x + (lane & 15), j = jb + 16 * y + 4 * (lane >> 4);
-                if (i < Jp) // the padding columns too (zero)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j + e < I)
-                            out[(j + e) * p.ld_out + i] = (uint16_t)(h[e >> 1] >> (16 * (e & 1)));
+            if (mirror) {
+                const uint32_t skip = (uint32_t)!(ib + 16 * x + (lane & 12) < Jp) << 31; // padding columns: zero
+                __builtin_amdgcn_raw_buffer_store_b64(
+                    transposed4(h, lane), mrs,
+                    (int)((mirror_off + 32 * y * (uint32_t)p.ld_out + 32 * x) | skip), 0, 0);
             }
             return h;
         });
@@ -270,13 +309,14 @@ __device__ __forceinline__ void store_small(const ProductParams &p, const Job &j
 
 // The last product, on the caller's matrices.  VEC: their rows take 4 elements at a time.
 template <class C, int STEP, bool VEC>
-__device__ __forceinline__ void store_last(const ProductParams &p, const Job &job, int ti, int tj, LB_LDS char *smem) {
+__device__ __forceinline__ void store_last(const ProductParams &p, const Job &job, int64_t b, int ti, int tj,
+                                           LB_LDS char *smem) {
     Acc<C> acc;
     accumulate<C>(job, ti, tj, smem, acc);
     const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
     const int64_t I = job.I, J = job.J;
-    const uint16_t *const add = p.add + blockIdx.y * p.step_add; // ld a multiple of 8, padded
-    const int64_t mine = blockIdx.y * I * J;
+    const uint16_t *const add = p.add + b * p.step_add; // ld a multiple of 8, padded
+    const int64_t mine = b * I * J;
     u32x2_t x[C::FJ];
     f32x4_t w[C::FJ];
     auto load = [&](int64_t i, int rows, int64_t j) {
@@ -354,18 +394,20 @@ __global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_
         return;
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
     LB_LDS char *smem = (LB_LDS char *)smem_raw;
+    const int u = gathered(blockIdx.x, gridDim.x); // over the whole batch
+    const int64_t b = u / p.tiles;
     Job job = p.job;
-    job.a += blockIdx.y * p.step_a;
-    job.b += blockIdx.y * p.step_b;
+    job.a += b * p.step_a;
+    job.b += b * p.step_b;
     int ti, tj;
     if constexpr ((STEP == GRAM || STEP == ADD) && FLAG)
-        coords_lower(job.tiles_i, blockIdx.x, ti, tj);
+        coords_lower(u - (int)b * p.tiles, ti, tj);
     else
-        coords(job, blockIdx.x, ti, tj);
+        coords(job, u - (int)b * p.tiles, ti, tj);
     if constexpr (STEP == GRAM || STEP == ADD)
-        store_small<C, STEP, FLAG>(p, job, ti, tj, smem);
+        store_small<C, STEP, FLAG>(p, job, b, ti, tj, smem);
     else
-        store_last<C, STEP, FLAG>(p, job, ti, tj, smem);
+        store_last<C, STEP, FLAG>(p, job, b, ti, tj, smem);
 }
 
 template <class C, int STEP, bool FLAG>
@@ -376,18 +418,29 @@ void launch(ProductParams &p, int64_t batch, hipStream_t s) {
     const int64_t tiles = (STEP == GRAM || STEP == ADD) && FLAG
                               ? (int64_t)p.job.tiles_i * (p.job.tiles_i + 1) / 2
                               : (int64_t)p.job.tiles_i * p.job.tiles_j;
-    hipLaunchKernelGGL((k_muon_product<C, STEP, FLAG>), dim3((unsigned)tiles, (unsigned)batch), dim3(kThreads), 0, s,
-                       p);
+    p.tiles = (int)tiles;
+    hipLaunchKernelGGL((k_muon_product<C, STEP, FLAG>), dim3((unsigned)(tiles * batch)), dim3(kThreads), 0, s, p);
 }
 template <bool AOC, bool BOC, int STEP, bool FLAG>
-void product(ProductParams &p, int64_t batch, hipStream_t s) {
-    const bool sym = (STEP == GRAM || STEP == ADD) && FLAG;
-    switch (muon::choose(batch, p.job.I, p.job.J, p.job.R, sym)) {
+void product_with(muon::Tile tile, ProductParams &p, int64_t batch, hipStream_t s) {
+    switch (tile) {
     case muon::TILE256: launch<Cfg<F16, 2, 2, 8, 8, AOC, BOC, 2, 3>, STEP, FLAG>(p, batch, s); break;
     case muon::TILE128: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 2>, STEP, FLAG>(p, batch, s); break;
     case muon::TILE128_DEEP: launch<Cfg<F16, 2, 2, 4, 4, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
     default: launch<Cfg<F16, 2, 2, 2, 2, AOC, BOC, 4>, STEP, FLAG>(p, batch, s); break;
     }
+}
+template <bool AOC, bool BOC, int STEP, bool FLAG>
+void product(ProductParams &p, int64_t batch, hipStream_t s) {
+    product_with<AOC, BOC, STEP, FLAG>(muon::choose(batch, p.job.I, p.job.J, p.job.R, false).tile, p, batch, s);
+}
+template <bool AOC, bool BOC, int STEP>
+void symmetric_product(ProductParams &p, int64_t batch, hipStream_t s) {
+    const muon::Choice c = muon::choose(batch, p.job.I, p.job.J, p.job.R, true);
+    if (c.lower)
+        product_with<AOC, BOC, STEP, true>(c.tile, p, batch, s);
+    else
+        product_with<AOC, BOC, STEP, false>(c.tile, p, batch, s);
 }
 // A and B = bA + cA² of a matrix whose shorter side fits one tile: the block writes A, in
 // fp16, to LDS as RC pairs (the ring is free by then), multiplies it by itself from there
@@ -451,7 +504,7 @@ __global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_
     }
     mfma_drain();
     __syncthreads(); // every wave has read A: the epilogue may stage over it
-    store16<C>(
+    store16<C, false>(
         acc, p.out + blockIdx.x * p.step_out, p.ld_out, job.I, (job.J + 7) / 8 * 8, (w / 2) * F * 16, (w % 2) * F * 16,
         true, smem, [](int) {},
         [&](int x, int y) {
@@ -475,13 +528,6 @@ void one_tile_poly(int T, ProductParams &p, float f2, int64_t batch, hipStream_t
                            p, f2);
 }
 
-template <bool AOC, bool BOC, int STEP>
-void symmetric_product(ProductParams &p, int64_t batch, hipStream_t s) {
-    if (muon::lower_only(batch, p.job.I, p.job.R))
-        product<AOC, BOC, STEP, true>(p, batch, s);
-    else
-        product<AOC, BOC, STEP, false>(p, batch, s);
-}
 template <int STEP>
 void last_product(ProductParams &p, int64_t batch, bool tall, bool vec, hipStream_t s) {
     if (tall)
@@ -493,7 +539,7 @@ void last_product(ProductParams &p, int64_t batch, bool tall, bool vec, hipStrea
 template <int GT>
 void prepare(PrepParams &p, int64_t batch, bool vec, hipStream_t s) {
     const dim3 norm((unsigned)p.parts, (unsigned)batch);
-    const dim3 scale((unsigned)std::min<int64_t>(cdiv(p.K * p.Np / 4, 256), 8 * muon::kCUs), (unsigned)batch);
+    const dim3 scale((unsigned)std::min<int64_t>(cdiv(p.K * p.Np / 8, 256), std::max<int64_t>(16 * muon::kCUs / batch, 64)), (unsigned)batch);
     if (vec) {
         hipLaunchKernelGGL((k_muon_norm<GT, true>), norm, dim3(256), 0, s, p);
         hipLaunchKernelGGL((k_muon_scale<GT, true>), scale, dim3(256), 0, s, p);

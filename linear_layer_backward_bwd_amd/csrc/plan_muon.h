@@ -23,44 +23,44 @@ inline int64_t tiles(int64_t batch, int64_t I, int64_t J, int T, bool sym) {
     const int64_t ti = cdiv(I, T), tj = cdiv(J, T);
     return batch * (sym ? ti * (ti + 1) / 2 : ti * tj);
 }
-// Microseconds of a launch: rounds of (fixed + per 64 reduction indices), from single
-// products on the card (64x64 to 4096x12288, R from 64 to 4096; a tile alone on its CU and
-// two to a CU): 256x256 7.5 + 1.03, 128x128 3.8 + 0.36 alone (the deep ring keeps it so)
-// and 0.65 two to a CU, 64x64 2.8 + 0.24 alone and 0.34.
+// Microseconds of a launch of n tiles, fixed + per 64 reduction indices, from the products
+// themselves on the card (sides 96 to 4096 over 256 to 12288, batches of 1 to 12, random
+// operands).  256x256: 8.4 + 1.04, rising to 1.4 with every CU at work (the power limit's
+// clock).  128x128, two to a CU: 5 + 0.57 for up to 256 tiles, 4.6 + 0.8 beyond; one to a CU
+// (a ring of four slots keeps it so): 4 + 0.36, rising to 0.54.  64x64: 2.8 + 0.25, 0.37 two
+// to a CU.  Tiles past whole rounds run as a launch of their own.
 inline double microseconds(Tile t, int64_t n, int64_t R) {
     const double p = (double)cdiv(R, 64);
+    const bool one = t == TILE256 || t == TILE128_DEEP; // to a CU
+    const int64_t slots = one ? kCUs : 2 * kCUs, rounds = n / slots, rem = n % slots;
+    const double share = (double)rem / kCUs;
+    double first, full, fixed, last; // a full round, and what is left
     switch (t) {
-    case TILE256: return cdiv(n, kCUs) * (7.5 + 1.03 * p);
-    case TILE128: return cdiv(n, 2 * kCUs) * (3.8 + 0.65 * p);
-    case TILE128_DEEP: return cdiv(n, kCUs) * (3.9 + 0.36 * p);
-    default: return n <= kCUs ? 2.8 + 0.24 * p : cdiv(n, 2 * kCUs) * (2.8 + 0.34 * p);
+    case TILE256: first = fixed = 8.4, full = 1.4, last = 1.04 + 0.36 * std::max(0.0, share - 0.5) * 2; break;
+    case TILE128: first = 4.6, full = 0.8, fixed = 5.0, last = rem <= kCUs ? 0.57 : 0.8; break;
+    case TILE128_DEEP: first = fixed = 4.0, full = 0.54, last = 0.36 + 0.18 * share; break;
+    default: first = fixed = 2.8, full = 0.37, last = rem <= kCUs ? 0.25 : 0.37; break;
     }
+    return rounds * (first + full * p) + (rem ? fixed + last * p : 0.0);
 }
-inline Tile choose(int64_t batch, int64_t I, int64_t J, int64_t R, bool sym, double *us = nullptr) {
-    Tile best = TILE256;
-    double least = 0;
-    for (Tile t : {TILE256, TILE128, TILE128_DEEP, TILE64}) {
-        const int T = t == TILE256 ? 256 : t == TILE64 ? 64 : 128;
-        const double c = microseconds(t, tiles(batch, I, J, T, sym), R);
-        if (t == TILE256 || c < least) {
-            best = t;
-            least = c;
+struct Choice {
+    Tile tile;
+    bool lower; // of a symmetric product: the tiles on and below the diagonal only
+    double us;
+};
+// The tiles on and below the diagonal of a symmetric product each store their mirror image
+// too: 7 us for 256x256 tiles, 2 for 128x128, 0.4 for 64x64.
+inline Choice choose(int64_t batch, int64_t I, int64_t J, int64_t R, bool symmetric) {
+    Choice best{TILE256, false, 1e30};
+    for (Tile t : {TILE256, TILE128, TILE128_DEEP, TILE64})
+        for (int lower = 0; lower <= (symmetric ? 1 : 0); ++lower) {
+            const int T = t == TILE256 ? 256 : t == TILE64 ? 64 : 128;
+            const double mirror = !lower ? 0.0 : t == TILE256 ? 7.0 : t == TILE64 ? 0.4 : 2.0;
+            const double c = microseconds(t, tiles(batch, I, J, T, lower), R) + mirror;
+            if (c < best.us)
+                best = Choice{t, lower != 0, c};
         }
-    }
-    if (us)
-        *us = least;
     return best;
-}
-
-// Symmetric products run their tiles on and below the diagonal only, each storing its
-// mirror image too (about 3 us: 16-bit stores), where that shortens the launch; at equal
-// rounds and long reductions too, as idle CUs leave the others a higher clock (4096 x 4096
-// over 12288: 136 tiles 272 us, all 256 300).
-inline bool lower_only(int64_t batch, int64_t I, int64_t R) {
-    double half, full;
-    choose(batch, I, I, R, true, &half);
-    choose(batch, I, I, R, false, &full);
-    return half + 3.0 < full || (half <= full && full > 40.0);
 }
 
 // A matrix whose shorter side fits one tile has A and B = bA + cA² made by one block in one
@@ -70,13 +70,13 @@ inline int one_tile(int64_t batch, int64_t s, int64_t R) {
         return 64;
     if (s > 128)
         return 0;
-    double us = 0;
-    choose(batch, s, s, R, false, &us);
-    return microseconds(TILE128_DEEP, batch, R) + 1.0 <= us + 3.3 ? 128 : 0;
+    return microseconds(TILE128_DEEP, batch, R) + 1.0 <= choose(batch, s, s, R, true).us + 3.5 ? 128 : 0;
 }
 
 struct Plan {
-    int64_t s, sp, Np; // shorter side, rounded up to 8; N rounded up to 8
+    // the shorter side; it and N rounded up to 64: rows of whole 128-byte lines (ragged rows
+    // cost a product a quarter of its time: every 128-byte fetch touched two lines)
+    int64_t s, sp, Np;
     bool tall;         // K > N: the products run on the columns
     int parts;
     int64_t off_x0, off_x1, off_a, off_b, off_part, bytes;
@@ -86,8 +86,8 @@ inline Plan plan(int64_t batch, int64_t K, int64_t N) {
     Plan p;
     p.tall = K > N;
     p.s = std::min(K, N);
-    p.sp = up(p.s, 8);
-    p.Np = up(N, 8);
+    p.sp = up(p.s, 64);
+    p.Np = up(N, 64);
     p.parts = (int)std::min<int64_t>({kMaxParts, cdiv(K * N, 4096), std::max<int64_t>(1, kNormBlocks / batch)});
     int64_t at = 0;
     auto take = [&](int64_t n) {

@@ -66,7 +66,7 @@ inline int64_t piece(int64_t V, int64_t per_col, int64_t cap) {
 
 struct Fwd {
     int rows;          // Rows
-    int64_t Kp;        // K rounded up to 8
+    int64_t Kp;        // rows of the copy of X: K rounded up to 64 (whole 128-byte lines)
     int64_t Vc;        // piece width
     int64_t parts;     // statistics entries (tiles) per row and piece
     int join_rows;     // rows per block that joins them
@@ -76,7 +76,7 @@ struct Fwd {
 inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     Fwd f;
     f.rows = choose_rows(M, K, V);
-    f.Kp = up(K, 8);
+    f.Kp = up(K, 64);
     const int64_t cols = shape(f.rows).tj;
     f.Vc = piece(V, cdiv(8 * M, cols), kPartBytes);
     if (pack_w)
@@ -166,7 +166,7 @@ inline int choose_both(int64_t M, int64_t Kp, int64_t Vc) {
 inline Bwd backward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     Bwd b;
     b.rows = choose_rows(M, K, V);
-    b.Kp = up(K, 8);
+    b.Kp = up(K, 64);
     b.Vc = piece(V, 2 * M, kGradBytes);
     if (pack_w)
         b.Vc = std::min(b.Vc, piece(V, 2 * K, kPackBytes));

@@ -126,13 +126,15 @@ __device__ __forceinline__ int swz_oc(int row) {
         return 2 * (((row >> 1) & 1) | (((row >> 3) & 1) << 1));
 }
 
-// Block index -> tile.  Blocks are dealt to the 8 XCDs in turn, so each XCD's blocks are
-// first gathered into one contiguous range (any count), then rastered in groups of
-// `group` tile rows, so that tiles that run together share operand panels in that XCD's L2.
-__device__ __forceinline__ void coords(const Job &jb, int t, int &ti, int &tj) {
-    const int n = jb.tiles_i * jb.tiles_j;
+// Blocks are dealt to the 8 XCDs in turn: block t of n -> its place when each XCD's blocks
+// are gathered into one contiguous range (any n), so that tiles that run together on an
+// XCD are neighbours and share operand panels in its L2.
+__device__ __forceinline__ int gathered(int t, int n) {
     const int x = t & 7, rem = n & 7;
-    int u = x * (n >> 3) + (x < rem ? x : rem) + (t >> 3);
+    return x * (n >> 3) + (x < rem ? x : rem) + (t >> 3);
+}
+// place -> tile, rastered in groups of `group` tile rows
+__device__ __forceinline__ void coords(const Job &jb, int u, int &ti, int &tj) {
     const int per = jb.group * jb.tiles_j;
     const int g = u / per;
     const int first = g * jb.group;
@@ -141,13 +143,9 @@ __device__ __forceinline__ void coords(const Job &jb, int t, int &ti, int &tj) {
     ti = first + u % rows;
     tj = u / rows;
 }
-
 // The same for a symmetric product: the tiles on and below the diagonal only (tj <= ti),
 // row by row.
-__device__ __forceinline__ void coords_lower(int tiles, int t, int &ti, int &tj) {
-    const int n = tiles * (tiles + 1) / 2;
-    const int x = t & 7, rem = n & 7;
-    const int u = x * (n >> 3) + (x < rem ? x : rem) + (t >> 3);
+__device__ __forceinline__ void coords_lower(int u, int &ti, int &tj) {
     ti = (int)((__builtin_sqrtf(8.0f * (float)u + 1.0f) - 1.0f) * 0.5f);
     while (ti * (ti + 1) / 2 > u)
         --ti;
@@ -486,15 +484,19 @@ __device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_L
 
 // 16-bit output through LDS: 32 rows of a wave at a time, whole 16-byte chunks per lane.
 // begin(h) is called before round h, value(x, y) gives the 4 packed values of acc[x][y].
-// vec: rows of dst 16-byte aligned and J a multiple of 8.
-template <class C, class Begin, class Fn>
-__device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, int64_t I, int64_t J, int64_t ib, int64_t jb,
-                                        bool vec, LB_LDS char *smem, Begin begin,
-                                        Fn value) {
+// vec: rows of dst 16-byte aligned and J a multiple of 8; stores then go through a
+// descriptor of the round's rows, which drops the rows past I without a branch (with a
+// check per store each became a branch of its own).  NT: data not read again soon.
+template <class C, bool NT, class Begin, class Fn>
+__device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, int64_t I, int64_t J, int64_t ib,
+                                        int64_t jb, bool vec, LB_LDS char *smem, Begin begin, Fn value) {
     constexpr int FJ = C::FJ, kRowB = FJ * 32, kChunks = 2 * FJ, kRows = 64 / kChunks;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     LB_LDS char *const reg = smem + w * (FJ * 1024);
+    const uint32_t off = (uint32_t)((lane / kChunks) * ld + 8 * (lane % kChunks)) * 2 |
+                         ((uint32_t)!(jb + 8 * (lane % kChunks) < J) << 31);
+    const uint32_t step = (uint32_t)(kRows * ld * 2);
 #pragma unroll
     for (int h = 0; h < C::FI / 2; ++h) {
         asm volatile("" ::: "memory"); // loads of later rounds stay behind this one's stores
@@ -519,13 +521,11 @@ __device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, 
                 v[q] = *reinterpret_cast<const LB_LDS u32x4_t *>(reg + r * kRowB + ((c ^ (r & (kChunks - 1))) << 4));
             }
             __builtin_amdgcn_sched_barrier(0); // all reads before the first store
-            const int64_t j = jb + 8 * (lane % kChunks);
+            const int64_t rows = max<int64_t>(0, min<int64_t>(32, I - i0));
+            const __amdgpu_buffer_rsrc_t rs = rsrc(dst + i0 * ld + jb, (uint32_t)(rows * ld * 2));
 #pragma unroll
-            for (int q = 0; q < FJ; ++q) {
-                const int64_t i = i0 + q * kRows + lane / kChunks;
-                if (i < I && j < J)
-                    __builtin_nontemporal_store(v[q], reinterpret_cast<u32x4_t *>(dst + i * ld + j));
-            }
+            for (int q = 0; q < FJ; ++q)
+                __builtin_amdgcn_raw_buffer_store_b128(v[q], rs, (int)(off + q * step), 0, NT ? 2 : 0);
         } else {
             // rows of any alignment: 64 lanes store 64 neighbouring elements
             for (int q = 0; q < 32 * FJ * 16 / 64; ++q) {

@@ -56,9 +56,16 @@ template <class Keep>
 __device__ __forceinline__ void pack_rows(const uint16_t *src, int64_t lds, int64_t rows, int64_t cols, uint16_t *dst,
                                           int64_t ldd, int64_t first, int64_t stride, Keep keep) {
     typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
-    const int64_t per = ldd / 8, n = rows * per;
-    for (int64_t i = first; i < n; i += stride) {
-        const int64_t r = i / per, c = (i - r * per) * 8;
+    const int64_t per = ldd / 8;
+    const int64_t step_r = stride / per, step_q = stride - step_r * per;
+    int64_t r = first / per, q = first - r * per; // one division, then steps
+    for (; r < rows; r += step_r, q += step_q) {
+        if (q >= per) {
+            q -= per;
+            if (++r >= rows)
+                break;
+        }
+        const int64_t c = q * 8;
         u32x4_t v = {};
         if (c < cols && keep(r)) {
             const uint16_t *p = src + r * lds + c;
@@ -159,7 +166,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_stats(S
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
     LB_LDS char *smem = (LB_LDS char *)smem_raw;
     int ti, tj;
-    coords(p.job, blockIdx.x, ti, tj);
+    coords(p.job, gathered(blockIdx.x, gridDim.x), ti, tj);
     Acc<C> acc;
     accumulate<C>(p.job, ti, tj, smem, acc);
     const int lane = threadIdx.x & 63;
@@ -405,7 +412,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(Gr
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
     LB_LDS char *smem = (LB_LDS char *)smem_raw;
     int ti, tj;
-    coords(p.job, blockIdx.x, ti, tj);
+    coords(p.job, gathered(blockIdx.x, gridDim.x), ti, tj);
     Acc<C> acc;
     accumulate<C>(p.job, ti, tj, smem, acc);
     const int lane = threadIdx.x & 63;
@@ -419,7 +426,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(Gr
         rp[x] = i < p.job.I ? p.row[i] : RowParam{0.0f, 0.0f, -1, 0};
     }
     const int j0 = (int)jb + 4 * (lane >> 4);
-    store16<C>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, smem, [](int) {}, [&](int x, int y) {
+    store16<C, false>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, smem, [](int) {}, [&](int x, int y) {
         const int t = rp[x].t < 0 ? -1 : rp[x].t - (int)p.v0;
         float g[4];
 #pragma unroll
@@ -456,6 +463,7 @@ struct BothParams {
 template <class C>
 __device__ __forceinline__ void dx_tile(const BothParams &p, int b, LB_LDS char *smem) {
     const int per = p.dx.tiles_i * p.dx.tiles_j;
+    b = gathered(b, p.dx_tiles); // neighbours share a range too
     const int sp = b / per;
     Job j = p.dx;
     const int64_t k0 = (int64_t)sp * p.split_len;
@@ -506,14 +514,14 @@ __device__ __forceinline__ void dx_tile(const BothParams &p, int b, LB_LDS char 
 template <class C>
 __device__ __forceinline__ void dw_tile(const BothParams &p, int b, LB_LDS char *smem) {
     int ti, tj;
-    coords(p.dw, b, ti, tj);
+    coords(p.dw, gathered(b, p.dw_tiles), ti, tj);
     Acc<C> acc;
     accumulate<C>(p.dw, ti, tj, smem, acc);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
     const float f = p.pow2[1];
-    store16<C>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, smem, [](int) {}, [&](int x, int y) {
+    store16<C, true>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, smem, [](int) {}, [&](int x, int y) {
         const f32x4_t &a = acc[x][y];
         return u32x2_t{C::T::pack2(a[0] * f, a[1] * f), C::T::pack2(a[2] * f, a[3] * f)};
     });
@@ -711,7 +719,9 @@ hipError_t forward(const XentArgs &a, hipStream_t s) {
     StatsParams p{};
     p.job.a = static_cast<const uint16_t *>(a.X);
     p.job.lda = a.K;
-    if (a.K % 8 != 0 || !aligned(a.X, 16)) {
+    // also where rows are no whole 128-byte lines and the product is large: ragged rows cost
+    // a quarter of its time
+    if (a.K % 8 != 0 || !aligned(a.X, 16) || (a.K % 64 != 0 && (double)a.M * a.K * a.V > 5e10)) {
         uint16_t *const x = reinterpret_cast<uint16_t *>(ws + f.off_x);
         pack(a.X, a.K, a.M, a.K, x, f.Kp, s);
         p.job.a = x;
