@@ -46,6 +46,13 @@ inline int choose_rows(int64_t M, int64_t K, int64_t V) {
     return best;
 }
 
+// Rows of W at any alignment (V no multiple of 8, or W not 16-byte aligned) are read as they
+// are, through registers, or copied to padded rows first.  The copy costs 0.75 ps an
+// element, reading as it is 18-28% of a product on 256x256 tiles: forward, M = 2048 776 us
+// against about 830, M = 6000 (K = 4096, V = 30001) 1330 against 1220.  Backward the two
+// products pay: M = 100 97 against 113, M = 777 697 against 614.
+inline bool pack_forward(int64_t M) { return M >= 2560; }
+inline bool pack_backward(int64_t M) { return M > 256; }
 // A packed copy of W's piece (V not a multiple of 8, or W not 16-byte aligned) takes at
 // most this.  Large pieces waste fewer part-filled rounds of tiles (pieces of 128 MiB,
 // which stay in the last-level cache, were slower).
@@ -155,10 +162,11 @@ inline double both_us(int64_t M, int64_t Kp, int64_t Vc, int both) {
     const double tx = x.fixed + x.full * px, tw = w.fixed + w.full * pw;
     return (nx * tx + nw * tw) / x.slots + 0.5 * std::max(tx, tw) + sums;
 }
+// (dX's 256x256 tile does not read W at any alignment: its epilogue would spill)
 inline int choose_both(int64_t M, int64_t Kp, int64_t Vc) {
     int best = X32_W128;
     for (int b : {X64_W128, X128_W128, X256_W256, X64_W64})
-        if (both_us(M, Kp, Vc, b) < both_us(M, Kp, Vc, best))
+        if ((b != X256_W256 || pack_backward(M)) && both_us(M, Kp, Vc, b) < both_us(M, Kp, Vc, best))
             best = b;
     return best;
 }
@@ -192,10 +200,10 @@ inline Bwd backward(int64_t M, int64_t K, int64_t V, bool pack_w) {
 
 // enough for any alignment of W
 inline int64_t forward_bytes(int64_t M, int64_t K, int64_t V) {
-    return std::max(forward(M, K, V, false).bytes, forward(M, K, V, true).bytes);
+    return std::max(forward(M, K, V, false).bytes, forward(M, K, V, pack_forward(M)).bytes);
 }
 inline int64_t backward_bytes(int64_t M, int64_t K, int64_t V) {
-    return std::max(backward(M, K, V, false).bytes, backward(M, K, V, true).bytes);
+    return std::max(backward(M, K, V, false).bytes, backward(M, K, V, pack_backward(M)).bytes);
 }
 
 } // namespace xent

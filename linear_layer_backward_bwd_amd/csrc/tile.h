@@ -66,11 +66,12 @@ struct F16 {
 };
 
 // Four waves as WI x WJ, each FI x FJ fragments of 16 x 16; S pair slots for A, SB for B.
-template <class T_, int WI_, int WJ_, int FI_, int FJ_, bool AOC_, bool BOC_, int S_, int SB_ = S_>
+// BANY: B's rows may start at any element (2-byte alignment): they come through registers.
+template <class T_, int WI_, int WJ_, int FI_, int FJ_, bool AOC_, bool BOC_, int S_, int SB_ = S_, bool BANY_ = false>
 struct Cfg {
     using T = T_;
     static constexpr int WI = WI_, WJ = WJ_, FI = FI_, FJ = FJ_, S = S_, SB = SB_;
-    static constexpr bool AOC = AOC_, BOC = BOC_;
+    static constexpr bool AOC = AOC_, BOC = BOC_, BANY = BANY_;
     static constexpr int TI = WI * FI * 16, TJ = WJ * FJ * 16;
     static constexpr int kPairA = TI * 128, kPairB = TJ * 128; // bytes of an operand's pair
     static constexpr int kOffB = S * kPairA;                   // A's slots first, then B's
@@ -82,16 +83,21 @@ struct Cfg {
     static_assert(!AOC || TI == 64 || TI == 128 || TI == 256, "OC rows of 128, 256 or 512 bytes");
     static_assert(!BOC || TJ == 64 || TJ == 128 || TJ == 256, "OC rows of 128, 256 or 512 bytes");
     static_assert(4 * FJ * 1024 <= kLds, "the epilogue stages 16 rows per wave in the ring");
-    // DMA instructions that may be in flight while the next pair has landed
-    static constexpr int kAhead = (S - 2) * kDma + (SB - S) * kDmaB;
+    // memory instructions that may be in flight while A's next pair (and B's, if it is
+    // DMA'd too) has landed; a chunk of B that comes through registers is two loads
+    static constexpr int kAhead =
+        BANY ? (S - 2) * (kDmaA + 2 * kDmaB) + 2 * kDmaB : (S - 2) * kDma + (SB - S) * kDmaB;
     static_assert(SB >= S && kAhead + kDma < 64, "vmcnt is 6 bits");
+    using With = Cfg<T_, WI_, WJ_, FI_, FJ_, AOC_, BOC_, S_, SB_, true>; // the same, B at any alignment
 };
 
 // One product.  lda, ldb multiples of 8 elements, a and b 16-byte aligned.  Operands are
 // fetched in 16-byte chunks along their contiguous index: where that extent (RC: R, OC: I
 // or J) is no multiple of 8, the rest of the last chunk is memory of the operand's own,
 // and zero (or only reaches sums that the epilogue drops).  2*256*ld < 2^31 for RC
-// operands and 2*64*ld < 2^31 for OC ones, checked on the host.
+// operands and 2*64*ld < 2^31 for OC ones, checked on the host.  With BANY, b and ldb are
+// free; what follows a row's end in its last chunk is then the next row (the columns of C
+// it reaches are dropped, or A is zero there).
 struct Job {
     const uint16_t *a, *b;
     int64_t lda, ldb;
@@ -221,6 +227,70 @@ struct Side {
     }
 };
 
+// The same for rows at any alignment of 2 bytes.  A 16-byte chunk is fetched as the aligned
+// dwords that hold it, four and one more, shifted together (a row's chunks all by 0 or by
+// 16 bits) and written to the ring by ds_write.  The stage holds the pair after those in
+// the ring, so a load has a pair's time to land.  No load passes the dword that holds the
+// matrix' last element.
+template <int T, bool OC, int kDmaN>
+struct AnySide {
+    uint32_t off[kDmaN], dst[kDmaN];
+    u32x4_t v[kDmaN];  // stage
+    uint32_t e[kDmaN]; // the fifth dwords
+    uint32_t shift;
+    const uint16_t *cur; // aligned down to a dword
+    int64_t step, left, ld, span;
+    int half, kchunk; // elements that aligning skipped back; RC: this lane's first r
+
+    __device__ __forceinline__ void init(const uint16_t *p, int64_t ld_, int64_t O, int64_t R, int64_t o0, int w,
+                                         int lane) {
+        ld = ld_;
+        left = R;
+        const uint16_t *first = OC ? p + o0 : p + o0 * ld;
+        half = (int)((reinterpret_cast<uintptr_t>(first) >> 1) & 1);
+        cur = first - half;
+        constexpr int kChunks = OC ? T / 8 : 8, kRows = 64 / kChunks; // per instruction
+        const int c = lane % kChunks;
+        kchunk = OC ? 0 : 8 * c;
+        step = OC ? 64 * ld : 64; // whole dwords: the shifts stay
+        span = OC ? O - o0 : min<int64_t>(T, O - o0);
+        shift = (uint32_t)((half + (lane / kChunks) * ld) & 1) * 16; // kRows is even
+#pragma unroll
+        for (int d = 0; d < kDmaN; ++d) {
+            const int row = (w * kDmaN + d) * kRows + lane / kChunks;
+            const bool in = OC ? 8 * c < span : row < span;
+            off[d] = ((uint32_t)((half + row * ld + 8 * c) * 2) & ~3u) | ((uint32_t)!in << 31);
+            dst[d] = (uint32_t)(row * (16 * kChunks) + ((c ^ (OC ? swz_oc<T>(row) : row & 7)) << 4));
+        }
+    }
+    struct Src {
+        __amdgpu_buffer_rsrc_t rs;
+        uint32_t mask;
+    };
+    __device__ __forceinline__ Src next() {
+        Src s;
+        const int64_t rows = OC ? min<int64_t>(64, left) : span;
+        const int64_t last = OC ? span : left; // elements of the last row
+        s.rs = rsrc(cur, left > 0 ? (uint32_t)((half + (rows - 1) * ld + last) * 2 + 3) & ~3u : 0u);
+        s.mask = OC ? 0u : (uint32_t)(kchunk >= left) << 31;
+        cur += step;
+        left -= 64;
+        return s;
+    }
+    __device__ __forceinline__ void load(const Src &s, int d) {
+        const int o = (int)(off[d] | s.mask);
+        v[d] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(s.rs, o, 0, 0));
+        e[d] = __builtin_amdgcn_raw_buffer_load_b32(s.rs, o + 16, 0, 0);
+    }
+    __device__ __forceinline__ void write(LB_LDS char *slot, int d) const {
+        u32x4_t x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x[k] = __builtin_amdgcn_alignbit(k == 3 ? e[d] : v[d][k + 1], v[d][k], shift);
+        asm volatile("ds_write_b128 %0, %1" ::"v"(slot + dst[d]), "v"(x) : "memory");
+    }
+};
+
 // LDS fragment addresses of one operand for a wave, and the reads.  Inline asm: the
 // compiler would wait for the DMA in flight (it may alias) before every read.  Callers
 // wait with settle(), which also keeps every output in use until the data has landed.
@@ -315,7 +385,7 @@ __device__ __forceinline__ void pin(f32x4_t (&a)[N]) {
 template <class C>
 __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS char *smem, Acc<C> &acc) {
     using SA = Side<C::TI, C::AOC, C::kDmaA, C::S>;
-    using SB = Side<C::TJ, C::BOC, C::kDmaB, C::SB>;
+    using SB = std::conditional_t<C::BANY, AnySide<C::TJ, C::BOC, C::kDmaB>, Side<C::TJ, C::BOC, C::kDmaB, C::SB>>;
     using FA = Frags<C::TI, C::AOC, C::FI, C::S>;
     using FB = Frags<C::TJ, C::BOC, C::FJ, C::SB>;
     constexpr int FI = C::FI, FJ = C::FJ, NM = FI * FJ;
@@ -343,10 +413,14 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
 
     // DMA instruction d of a pair: A's, then B's (which may have a slot more, and time)
     auto issue = [&](const typename SA::Src &xa, const typename SB::Src &xb, int slot_a, int slot_b, int d) {
-        if (d < C::kDmaA)
+        if (d < C::kDmaA) {
             sa.dma(xa, smem + slot_a * C::kPairA, w, d);
-        else
+        } else if constexpr (C::BANY) { // the staged pair to its slot, the one after it to the stage
+            sb.write(smem + C::kOffB + slot_b * C::kPairB, d - C::kDmaA);
+            sb.load(xb, d - C::kDmaA);
+        } else {
             sb.dma(xb, smem + C::kOffB + slot_b * C::kPairB, w, d - C::kDmaA);
+        }
     };
     auto settle = [&](u32x4_t (&af)[FI], u32x4_t (&bf)[FJ]) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -388,6 +462,12 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
     // prologue: every slot on its way; the first slab's fragments
     typename SA::Src xa;
     typename SB::Src xb;
+    if constexpr (C::BANY) {
+        xb = sb.next();
+#pragma unroll
+        for (int d = 0; d < C::kDmaB; ++d)
+            sb.load(xb, d);
+    }
 #pragma unroll
     for (int s = 0; s < C::SB; ++s) {
         if (s < C::S)
@@ -397,7 +477,7 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
         for (int d = s < C::S ? 0 : C::kDmaA; d < C::kDma; ++d)
             issue(xa, xb, s, s, d);
     }
-    vm_wait<C::kAhead + C::kDma>();
+    vm_wait<C::BANY ? 2 * C::kDmaB : C::kAhead + C::kDma>();
     ring_barrier();
 #pragma unroll
     for (int k = 0; k < FA::kReads; ++k)

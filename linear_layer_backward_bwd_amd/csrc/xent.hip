@@ -318,20 +318,34 @@ void set_tiles(Job &j) {
     j.group = 4;
 }
 
+// the tile, with B = W at any alignment if `any`
+template <class C, class Fn>
+void with_alignment(bool any, Fn fn) {
+    if (any)
+        fn(typename C::With{});
+    else
+        fn(C{});
+}
+
 template <class C>
 void run_stats(StatsParams &p, hipStream_t s) {
     set_tiles<C>(p.job);
     hipLaunchKernelGGL((k_xent_stats<C>), dim3((unsigned)(p.job.tiles_i * p.job.tiles_j)), dim3(kThreads), 0, s, p);
 }
 
-template <class T>
-void stats(int rows, StatsParams &p, hipStream_t s) {
+// fn(Cfg): the logits' tile
+template <class T, class Fn>
+void logits_tile(int rows, bool any, Fn fn) {
     switch (rows) {
-    case xent::ROWS32: run_stats<typename FwdCfg<T, xent::ROWS32>::C>(p, s); break;
-    case xent::ROWS64: run_stats<typename FwdCfg<T, xent::ROWS64>::C>(p, s); break;
-    case xent::ROWS128: run_stats<typename FwdCfg<T, xent::ROWS128>::C>(p, s); break;
-    default: run_stats<typename FwdCfg<T, xent::ROWS256>::C>(p, s); break;
+    case xent::ROWS32: with_alignment<typename FwdCfg<T, xent::ROWS32>::C>(any, fn); break;
+    case xent::ROWS64: with_alignment<typename FwdCfg<T, xent::ROWS64>::C>(any, fn); break;
+    case xent::ROWS128: with_alignment<typename FwdCfg<T, xent::ROWS128>::C>(any, fn); break;
+    default: with_alignment<typename FwdCfg<T, xent::ROWS256>::C>(any, fn); break;
     }
+}
+template <class T>
+void stats(int rows, bool any, StatsParams &p, hipStream_t s) {
+    logits_tile<T>(rows, any, [&](auto c) { run_stats<decltype(c)>(p, s); });
 }
 
 bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -606,18 +620,11 @@ void run_grad(GradParams &g, hipStream_t s) {
     hipLaunchKernelGGL((k_xent_grad<C>), dim3((unsigned)(g.job.tiles_i * g.job.tiles_j)), dim3(kThreads), 0, s, g);
 }
 template <class T>
-void grad(int rows, GradParams &g, hipStream_t s) {
-    switch (rows) {
-    case xent::ROWS32: run_grad<typename FwdCfg<T, xent::ROWS32>::C>(g, s); break;
-    case xent::ROWS64: run_grad<typename FwdCfg<T, xent::ROWS64>::C>(g, s); break;
-    case xent::ROWS128: run_grad<typename FwdCfg<T, xent::ROWS128>::C>(g, s); break;
-    default: run_grad<typename FwdCfg<T, xent::ROWS256>::C>(g, s); break;
-    }
+void grad(int rows, bool any, GradParams &g, hipStream_t s) {
+    logits_tile<T>(rows, any, [&](auto c) { run_grad<decltype(c)>(g, s); });
 }
-template <class T, int BOTH>
+template <class CX, class CW>
 void run_both(BothParams &p, hipStream_t s) {
-    using CX = typename BwdCfg<T, BOTH>::X;
-    using CW = typename BwdCfg<T, BOTH>::W;
     set_tiles<CX>(p.dx);
     set_tiles<CW>(p.dw);
     p.dx_tiles = p.want_dx ? p.dx.tiles_i * p.dx.tiles_j * p.splits : 0;
@@ -625,20 +632,27 @@ void run_both(BothParams &p, hipStream_t s) {
     p.dx_first = p.split_len * CX::TI * CX::TJ >= p.dw.R * CW::TI * CW::TJ;
     hipLaunchKernelGGL((k_xent_both<CX, CW>), dim3((unsigned)(p.dx_tiles + p.dw_tiles)), dim3(kThreads), 0, s, p);
 }
+template <class T, int BOTH>
+void both_as(bool any, BothParams &p, hipStream_t s) {
+    with_alignment<typename BwdCfg<T, BOTH>::X>(
+        any, [&](auto c) { run_both<decltype(c), typename BwdCfg<T, BOTH>::W>(p, s); });
+}
 template <class T>
-void both(int which, BothParams &p, hipStream_t s) {
+void both(int which, bool any, BothParams &p, hipStream_t s) {
     switch (which) {
-    case xent::X32_W128: run_both<T, xent::X32_W128>(p, s); break;
-    case xent::X64_W128: run_both<T, xent::X64_W128>(p, s); break;
-    case xent::X128_W128: run_both<T, xent::X128_W128>(p, s); break;
-    case xent::X256_W256: run_both<T, xent::X256_W256>(p, s); break;
-    default: run_both<T, xent::X64_W64>(p, s); break;
+    case xent::X32_W128: both_as<T, xent::X32_W128>(any, p, s); break;
+    case xent::X64_W128: both_as<T, xent::X64_W128>(any, p, s); break;
+    case xent::X128_W128: both_as<T, xent::X128_W128>(any, p, s); break;
+    case xent::X256_W256: // never with `any`
+        run_both<typename BwdCfg<T, xent::X256_W256>::X, typename BwdCfg<T, xent::X256_W256>::W>(p, s);
+        break;
+    default: both_as<T, xent::X64_W64>(any, p, s); break;
     }
 }
 
 template <class T>
 hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
-    const bool pack_w = a.V % 8 != 0 || !aligned(a.W, 16);
+    const bool ragged = a.V % 8 != 0 || !aligned(a.W, 16), pack_w = ragged && xent::pack_backward(a.M);
     const xent::Bwd b = xent::backward(a.M, a.K, a.V, pack_w);
     char *const ws = static_cast<char *>(a.ws);
     RowParam *const row = reinterpret_cast<RowParam *>(ws + b.off_row);
@@ -699,8 +713,8 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
         p.dw_vec = a.V % 8 == 0 && aligned(a.dW, 16);
         p.pow2 = pow2;
         p.want_dx = a.dX != nullptr;
-        grad<T>(b.rows, g, s);
-        both<T>(b.both, p, s);
+        grad<T>(b.rows, ragged && !pack_w, g, s);
+        both<T>(b.both, ragged && !pack_w, p, s);
     }
     if (a.dX && b.splits > 1) {
         const int64_t blocks = std::min<int64_t>(cdiv(a.M * b.Kp / 4, 64), 32 * xent::kCUs);
@@ -713,7 +727,7 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
 
 template <class T>
 hipError_t forward(const XentArgs &a, hipStream_t s) {
-    const bool pack_w = a.V % 8 != 0 || !aligned(a.W, 16);
+    const bool ragged = a.V % 8 != 0 || !aligned(a.W, 16), pack_w = ragged && xent::pack_forward(a.M);
     const xent::Fwd f = xent::forward(a.M, a.K, a.V, pack_w);
     char *const ws = static_cast<char *>(a.ws);
     StatsParams p{};
@@ -758,7 +772,7 @@ hipError_t forward(const XentArgs &a, hipStream_t s) {
         p.job.b = w;
         p.job.J = vc;
         p.v0 = v0;
-        stats<T>(f.rows, p, s);
+        stats<T>(f.rows, ragged && !pack_w, p, s);
         j.parts = cdiv(vc, xent::shape(f.rows).tj);
         j.first = v0 == 0;
         j.last = v0 + f.Vc >= a.V;

@@ -154,6 +154,18 @@ def test_unaligned(M, K, V, dtype, offset):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,K,V", [(1, 130, 333), (17, 64, 4097), (70, 96, 1027), (130, 520, 2051), (200, 64, 20001),
+                                   (256, 40, 9001), (257, 72, 1025), (2570, 64, 515), (2559, 65, 517)])
+def test_odd_vocabulary(M, K, V, dtype):
+    """Rows of W that start at any element: read through registers (M up to 256 backward, 2559
+    forward) or copied first, in each tile shape."""
+    X, W, t = case(M, K, V, dtype, seed=16)
+    loss, lse, out, dX, dW = both(X, W, t, dtype)
+    check_forward(X, W, t, (loss, lse, out))
+    check_backward(X, W, t, lse, dX, dW, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("M", [20, 400])
 def test_scales(M, dtype):
     """Loss scale, device scale (the forward's 1 / count) and row weights, some of them 0 or negative."""
