@@ -445,8 +445,11 @@ void symmetric_product(ProductParams &p, int64_t batch, hipStream_t s) {
 // A and B = bA + cA² of a matrix whose shorter side fits one tile: the block writes A, in
 // fp16, to LDS as RC pairs (the ring is free by then), multiplies it by itself from there
 // and adds bA from its own registers.  Neither A nor a second launch touches memory.
-template <class C>
-__global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_poly(ProductParams p, float f2) {
+// PARTS: A's sums come from `sums`, p.tiles ranges per matrix (k_muon_gram_part), added in
+// range order.
+template <class C, bool PARTS>
+__global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_poly(ProductParams p, float f2,
+                                                                                     const f32x4_t *sums) {
     static_assert(C::TI == C::TJ && C::FI == C::FJ && C::WI == 2, "one square tile");
     if (p.skip && *p.skip)
         return;
@@ -456,10 +459,23 @@ __global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Job job = p.job;
-    job.a += blockIdx.x * p.step_a;
-    job.b += blockIdx.x * p.step_b;
     Acc<C> acc;
-    accumulate<C>(job, 0, 0, smem, acc);
+    if constexpr (PARTS) {
+#pragma unroll
+        for (int x = 0; x < F; ++x)
+#pragma unroll
+            for (int y = 0; y < F; ++y) {
+                const f32x4_t *q = sums + ((int64_t)blockIdx.x * p.tiles * F * F + x * F + y) * 256 + threadIdx.x;
+                f32x4_t t = *q;
+                for (int r = 1; r < p.tiles; ++r)
+                    t += q[(int64_t)r * F * F * 256];
+                acc[x][y] = t;
+            }
+    } else {
+        job.a += blockIdx.x * p.step_a;
+        job.b += blockIdx.x * p.step_b;
+        accumulate<C>(job, 0, 0, smem, acc);
+    }
     // A as T/64 pairs of T rows of 128 bytes, chunk c of row o at c ^ (o % 8)
     u32x2_t a[F][F];
 #pragma unroll
@@ -517,15 +533,52 @@ __global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_
         });
 }
 
+// One range of that tile's reduction: its sums in fragment order, 16 bytes a lane.
+template <class C>
+__global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_gram_part(ProductParams p, int64_t len,
+                                                                                          f32x4_t *sums) {
+    if (p.skip && *p.skip)
+        return;
+    __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
+    constexpr int F = C::FI;
+    Job job = p.job;
+    const int64_t r0 = blockIdx.x * len; // a multiple of 64
+    job.a += blockIdx.y * p.step_a + (C::AOC ? r0 * job.lda : r0);
+    job.b = job.a;
+    job.R = min<int64_t>(len, p.job.R - r0);
+    Acc<C> acc;
+    accumulate<C>(job, 0, 0, (LB_LDS char *)smem_raw, acc);
+    f32x4_t *const q = sums + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * F * F * 256 + threadIdx.x;
+#pragma unroll
+    for (int x = 0; x < F; ++x) {
+        pin(acc[x]);
+#pragma unroll
+        for (int y = 0; y < F; ++y)
+            q[(x * F + y) * 256] = acc[x][y];
+    }
+}
+
+template <class C>
+void one_tile_as(int splits, ProductParams &p, float f2, f32x4_t *sums, int64_t batch, hipStream_t s) {
+    if (splits > 1) {
+        const int64_t len = muon::up(cdiv(p.job.R, splits), 64);
+        p.tiles = (int)cdiv(p.job.R, len);
+        hipLaunchKernelGGL((k_muon_gram_part<C>), dim3((unsigned)p.tiles, (unsigned)batch), dim3(kThreads), 0, s, p,
+                           len, sums);
+        hipLaunchKernelGGL((k_muon_poly<C, true>), dim3((unsigned)batch), dim3(kThreads), 0, s, p, f2,
+                           (const f32x4_t *)sums);
+    } else {
+        hipLaunchKernelGGL((k_muon_poly<C, false>), dim3((unsigned)batch), dim3(kThreads), 0, s, p, f2,
+                           (const f32x4_t *)nullptr);
+    }
+}
 template <bool OC>
-void one_tile_poly(int T, ProductParams &p, float f2, int64_t batch, hipStream_t s) {
+void one_tile_poly(const muon::Plan &pl, ProductParams &p, float f2, f32x4_t *sums, int64_t batch, hipStream_t s) {
     p.job.tiles_i = p.job.tiles_j = p.job.group = 1;
-    if (T == 64)
-        hipLaunchKernelGGL((k_muon_poly<Cfg<F16, 2, 2, 2, 2, OC, OC, 4>>), dim3((unsigned)batch), dim3(kThreads), 0, s,
-                           p, f2);
+    if (pl.one == 64)
+        one_tile_as<Cfg<F16, 2, 2, 2, 2, OC, OC, 4>>(pl.splits, p, f2, sums, batch, s);
     else
-        hipLaunchKernelGGL((k_muon_poly<Cfg<F16, 2, 2, 4, 4, OC, OC, 4>>), dim3((unsigned)batch), dim3(kThreads), 0, s,
-                           p, f2);
+        one_tile_as<Cfg<F16, 2, 2, 4, 4, OC, OC, 4>>(pl.splits, p, f2, sums, batch, s);
 }
 
 template <int STEP>
@@ -604,19 +657,19 @@ hipError_t launch_muon(const MuonArgs &a, hipStream_t s) {
     upd.scale = a.scale;
     upd.wd = a.wd;
     upd.skip = a.skip;
-    const int one = muon::one_tile(a.batch, pl.s, gram.job.R);
+    f32x4_t *const sums = reinterpret_cast<f32x4_t *>(ws + pl.off_sums);
     for (int t = 0; t < a.steps; ++t) {
         gram.job.a = gram.job.b = x;
-        if (one) { // A stays in LDS, B comes out
+        if (pl.one) { // A stays in LDS, B comes out
             gram.fa = kB;
             gram.out = gb;
-            pl.tall ? one_tile_poly<true>(one, gram, poly.f, a.batch, s)
-                    : one_tile_poly<false>(one, gram, poly.f, a.batch, s);
+            pl.tall ? one_tile_poly<true>(pl, gram, poly.f, sums, a.batch, s)
+                    : one_tile_poly<false>(pl, gram, poly.f, sums, a.batch, s);
         } else if (pl.tall)
             symmetric_product<true, true, GRAM>(gram, a.batch, s);
         else
             symmetric_product<false, false, GRAM>(gram, a.batch, s);
-        if (!one)
+        if (!pl.one)
             symmetric_product<false, false, ADD>(poly, a.batch, s);
         const bool last = t + 1 == a.steps;
         upd.job.a = pl.tall ? x : gb;

@@ -73,13 +73,31 @@ inline int one_tile(int64_t batch, int64_t s, int64_t R) {
     return microseconds(TILE128_DEEP, batch, R) + 1.0 <= choose(batch, s, s, R, true).us + 3.5 ? 128 : 0;
 }
 
+// The reduction of that one tile in ranges, one block each, where it is long: their fp32
+// sums are added by the block that makes B, a launch more (4.5 us) and 0.25 us a range.
+constexpr int kMaxSplits = 16;
+inline int one_tile_splits(int64_t batch, int T, int64_t R) {
+    const Tile t = T == 64 ? TILE64 : TILE128_DEEP;
+    int best = 1;
+    double least = microseconds(t, batch, R);
+    for (int s = 2; s <= kMaxSplits; s *= 2) {
+        const double c = microseconds(t, batch * s, cdiv(R, s)) + 4.5 + 0.25 * s * (T / 64);
+        if (c < least) {
+            best = s;
+            least = c;
+        }
+    }
+    return best;
+}
+
 struct Plan {
     // the shorter side; it and N rounded up to 64: rows of whole 128-byte lines (ragged rows
     // cost a product a quarter of its time: every 128-byte fetch touched two lines)
     int64_t s, sp, Np;
     bool tall;         // K > N: the products run on the columns
     int parts;
-    int64_t off_x0, off_x1, off_a, off_b, off_part, bytes;
+    int one, splits; // one_tile() and its ranges (1: none)
+    int64_t off_x0, off_x1, off_a, off_b, off_part, off_sums, bytes;
 };
 
 inline Plan plan(int64_t batch, int64_t K, int64_t N) {
@@ -100,6 +118,10 @@ inline Plan plan(int64_t batch, int64_t K, int64_t N) {
     p.off_a = take(2 * batch * p.s * p.sp);
     p.off_b = take(2 * batch * p.s * p.sp);
     p.off_part = take(8 * batch * p.parts);
+    const int64_t R = std::max(K, N);
+    p.one = one_tile(batch, p.s, R);
+    p.splits = p.one ? one_tile_splits(batch, p.one, R) : 1;
+    p.off_sums = take(p.splits > 1 ? 4 * batch * p.splits * p.one * p.one : 0);
     p.bytes = at;
     return p;
 }

@@ -607,14 +607,30 @@ __device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, 
             for (int q = 0; q < FJ; ++q)
                 __builtin_amdgcn_raw_buffer_store_b128(v[q], rs, (int)(off + q * step), 0, NT ? 2 : 0);
         } else {
-            // rows of any alignment: 64 lanes store 64 neighbouring elements
-            for (int q = 0; q < 32 * FJ * 16 / 64; ++q) {
-                const int e = q * 64 + lane;
-                const int r = e / (FJ * 16), c = e % (FJ * 16);
-                const uint16_t v = *reinterpret_cast<const LB_LDS uint16_t *>(
-                    reg + r * kRowB + (((c >> 3) ^ (r & (kChunks - 1))) << 4) + (c & 7) * 2);
-                if (i0 + r < I && jb + c < J)
-                    dst[(i0 + r) * ld + jb + c] = v;
+            // rows of any alignment: 64 lanes store 64 neighbouring elements of a row (two
+            // rows of 32), eight stores at a time
+            constexpr int kCols = FJ * 16, kSegs = kCols >= 64 ? kCols / 64 : 1, kPer = kCols >= 64 ? 1 : 64 / kCols;
+            const int64_t rows = max<int64_t>(0, min<int64_t>(32, I - i0));
+            const __amdgpu_buffer_rsrc_t rs =
+                rsrc(dst + i0 * ld + jb, rows && jb < J ? (uint32_t)(((rows - 1) * ld + J - jb) * 2) : 0u);
+            const int lr = lane / kCols, lc = lane % kCols; // lr = 0 for whole rows
+#pragma unroll
+            for (int q0 = 0; q0 < 32 * kSegs / kPer; q0 += 8) {
+                uint16_t v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int r = (q0 + u) / kSegs * kPer + lr, c = (q0 + u) % kSegs * 64 + lc;
+                    v[u] = *reinterpret_cast<const LB_LDS uint16_t *>(
+                        reg + r * kRowB + (((c >> 3) ^ (r & (kChunks - 1))) << 4) + (c & 7) * 2);
+                }
+                __builtin_amdgcn_sched_barrier(0); // all reads before the first store
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int r = (q0 + u) / kSegs * kPer, c = (q0 + u) % kSegs * 64;
+                    const uint32_t o = (uint32_t)(lr * ld + lc + c) * 2 + (uint32_t)(r * ld * 2);
+                    __builtin_amdgcn_raw_buffer_store_b16(
+                        v[u], rs, (int)(o | ((uint32_t)!(jb + c + lc < J) << 31)), 0, NT ? 2 : 0);
+                }
             }
         }
     }

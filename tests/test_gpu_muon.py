@@ -88,7 +88,7 @@ def check_orth(got, G, h=0.0, steps=5):
 
 SHAPES = [(1, 1, 1), (1, 1, 7), (1, 9, 1), (2, 5, 3), (3, 16, 40), (1, 64, 64), (3, 130, 70), (2, 33, 257),
           (1, 128, 128), (1, 256, 256), (2, 300, 1001), (2, 515, 300), (1, 129, 2056), (1, 1024, 1024),
-          (1, 2050, 515), (9, 256, 512), (150, 40, 48)]
+          (1, 2050, 515), (9, 256, 512), (150, 40, 48), (2, 4001, 48), (1, 100, 5000), (1, 5000, 128)]
 
 
 @pytest.mark.parametrize("gtype", ["f32", "f16", "bf16"])
