@@ -53,10 +53,11 @@ inline int choose_rows(int64_t M, int64_t K, int64_t V) {
 // products pay: M = 100 97 against 113, M = 777 697 against 614.
 inline bool pack_forward(int64_t M) { return M >= 2560; }
 inline bool pack_backward(int64_t M) { return M > 256; }
-// A packed copy of W's piece (V not a multiple of 8, or W not 16-byte aligned) takes at
-// most this.  Large pieces waste fewer part-filled rounds of tiles (pieces of 128 MiB,
-// which stay in the last-level cache, were slower).
-constexpr int64_t kPackBytes = (int64_t)1 << 30;
+// The copy of W's piece takes at most this.  Large pieces waste fewer part-filled rounds of
+// tiles (M = 2048, K = 4096, V = 50257 backward in pieces of 128 MiB 2559 us, whole 2387);
+// where V is a multiple of 8 only a pointer off 16 bytes needs the copy, and every call's
+// workspace has room for it: 128 MiB.
+inline int64_t pack_bytes(int64_t V) { return V % 8 == 0 ? (int64_t)128 << 20 : (int64_t)1 << 30; }
 // per-tile softmax statistics of a forward piece
 constexpr int64_t kPartBytes = (int64_t)128 << 20;
 // the piece of dL/dlogits (16 bit) that the backward pass holds
@@ -87,7 +88,7 @@ inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     const int64_t cols = shape(f.rows).tj;
     f.Vc = piece(V, cdiv(8 * M, cols), kPartBytes);
     if (pack_w)
-        f.Vc = std::min(f.Vc, piece(V, 2 * K, kPackBytes));
+        f.Vc = std::min(f.Vc, piece(V, 2 * K, pack_bytes(V)));
     f.parts = cdiv(f.Vc, cols);
     f.join_rows = M <= 4096 ? 16 : 64;
     if (M <= 32)
@@ -177,7 +178,7 @@ inline Bwd backward(int64_t M, int64_t K, int64_t V, bool pack_w) {
     b.Kp = up(K, 64);
     b.Vc = piece(V, 2 * M, kGradBytes);
     if (pack_w)
-        b.Vc = std::min(b.Vc, piece(V, 2 * K, kPackBytes));
+        b.Vc = std::min(b.Vc, piece(V, 2 * K, pack_bytes(V)));
     b.both = choose_both(M, b.Kp, b.Vc);
     b.splits = dx_splits(M, b.Kp, b.Vc, b.both);
     b.split_len = up(cdiv(b.Vc, b.splits), 64);

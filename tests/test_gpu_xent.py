@@ -145,7 +145,7 @@ def test_matches_float64(M, K, V, dtype):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("offset", [1, 2, 4])
-@pytest.mark.parametrize("M,K,V", [(3, 64, 264), (40, 40, 520), (300, 136, 512)])
+@pytest.mark.parametrize("M,K,V", [(3, 64, 264), (40, 40, 520), (300, 136, 512), (2600, 64, 264)])
 def test_unaligned(M, K, V, dtype, offset):
     X, W, t = case(M, K, V, dtype, offset=offset)
     loss, lse, out, dX, dW = both(X, W, t, dtype, offset=offset)
