@@ -274,8 +274,8 @@ __device__ __forceinline__ void store_small(const ProductParams &p, const Job &j
     const __amdgpu_buffer_rsrc_t mrs = rsrc(out + jb * p.ld_out + ib, (uint32_t)(mrows * p.ld_out * 2));
     const uint32_t mirror_off =
         (uint32_t)((4 * (lane >> 4) + mirror_row(lane)) * p.ld_out + (lane & 12)) * 2;
-    store16<C, false>(
-        acc, out, p.ld_out, I, Jp, ib, jb, true, smem,
+    store16<C>(
+        acc, out, p.ld_out, I, Jp, ib, jb, true, false, smem,
         [&](int h) {
 #pragma unroll
             for (int xx = 0; xx < 2; ++xx)
@@ -520,9 +520,9 @@ __global__ __launch_bounds__(kThreads, C::kLds > 80 * 1024 ? 1 : 2) void k_muon_
     }
     mfma_drain();
     __syncthreads(); // every wave has read A: the epilogue may stage over it
-    store16<C, false>(
+    store16<C>(
         acc, p.out + blockIdx.x * p.step_out, p.ld_out, job.I, (job.J + 7) / 8 * 8, (w / 2) * F * 16, (w % 2) * F * 16,
-        true, smem, [](int) {},
+        true, false, smem, [](int) {},
         [&](int x, int y) {
             const f32x4_t old = f16x4(a[x][y]);
             f32x4_t t;

@@ -21,14 +21,16 @@ struct Shape {
     int ti, tj, slots;
     double fixed, alone, full;
 };
-enum Rows { ROWS32 = 0, ROWS64 = 1, ROWS128 = 2, ROWS256 = 3, SQUARE64 = 4 };
+enum Rows { ROWS32 = 0, ROWS64 = 1, ROWS128 = 2, ROWS256 = 3, SQUARE64 = 4, WIDE64 = 5 };
 inline Shape shape(int r) {
     switch (r) {
     case ROWS32: return {32, 128, 2 * kCUs, 2.9, 0.25, 0.45};
     case ROWS64: return {64, 128, 2 * kCUs, 3.1, 0.30, 0.57};
     case ROWS128: return {128, 128, 2 * kCUs, 3.8, 0.36, 0.65};
     case ROWS256: return {256, 256, kCUs, 11.0, 1.03, 1.03};
-    default: return {64, 64, 2 * kCUs, 2.8, 0.24, 0.34};
+    case SQUARE64: return {64, 64, 2 * kCUs, 2.8, 0.24, 0.34};
+    default: return {64, 256, 3 * kCUs, 5.0, 0.30, 0.60}; // a reduction of at most 64
+
     }
 }
 inline int64_t tiles(int r, int64_t I, int64_t J) { return cdiv(I, shape(r).ti) * cdiv(J, shape(r).tj); }
@@ -113,16 +115,21 @@ inline Fwd forward(int64_t M, int64_t K, int64_t V, bool pack_w) {
 // The tiles of dX (rows of X by K, over a piece of Vc columns, in ranges) and dW (K by Vc,
 // over the rows) share a launch.
 struct Pair {
-    int x, w; // Rows
+    int x, w;  // Rows
+    int slots; // blocks of the launch on the card
 };
-enum Both { X32_W128 = 0, X64_W128 = 1, X128_W128 = 2, X256_W256 = 3, X64_W64 = 4 };
+// X32_ONCE and X64_ONCE: up to 64 rows, where dW is bound by writing it.  Its tiles take
+// their whole reduction at once, and small rings let three blocks share a CU (M = 15,
+// K = 1792, V = 109976: 267 us with 128x128 tiles, two to a CU).
+enum Both { X32_ONCE = 0, X64_ONCE = 1, X128_W128 = 2, X256_W256 = 3, X64_W64 = 4, X64_W128 = 5 };
 inline Pair pair(int both) {
     switch (both) {
-    case X32_W128: return {ROWS32, ROWS128};
-    case X64_W128: return {ROWS64, ROWS128};
-    case X128_W128: return {ROWS128, ROWS128};
-    case X256_W256: return {ROWS256, ROWS256};
-    default: return {SQUARE64, SQUARE64};
+    case X32_ONCE: return {ROWS32, WIDE64, 3 * kCUs};
+    case X64_ONCE: return {ROWS64, WIDE64, 3 * kCUs};
+    case X128_W128: return {ROWS128, ROWS128, 2 * kCUs};
+    case X256_W256: return {ROWS256, ROWS256, kCUs};
+    case X64_W128: return {ROWS64, ROWS128, 2 * kCUs};
+    default: return {SQUARE64, SQUARE64, 2 * kCUs};
     }
 }
 
@@ -144,7 +151,7 @@ inline int dx_splits(int64_t M, int64_t Kp, int64_t Vc, int both) {
     const int64_t ntx = tiles(c.x, M, Kp), ntw = tiles(c.w, Kp, Vc);
     const Shape x = shape(c.x), w = shape(c.w);
     const int64_t px = cdiv(Vc, 64), pw = cdiv(M, 64);
-    const double per_slot = (ntx * (px * x.full) + ntw * (pw * w.full + w.fixed)) / x.slots;
+    const double per_slot = (ntx * (px * x.full) + ntw * (pw * w.full + w.fixed)) / c.slots;
     const int64_t target = std::max<int64_t>(8, (int64_t)(per_slot / 2 / x.full));
     int64_t s = cdiv(px, target);
     s = std::min<int64_t>(s, std::max<int64_t>(1, kSplitBytes / (4 * M * Kp)));
@@ -161,13 +168,14 @@ inline double both_us(int64_t M, int64_t Kp, int64_t Vc, int both) {
     if (nx + nw <= kCUs)
         return std::max(x.fixed + x.alone * px, w.fixed + w.alone * pw) + sums;
     const double tx = x.fixed + x.full * px, tw = w.fixed + w.full * pw;
-    return (nx * tx + nw * tw) / x.slots + 0.5 * std::max(tx, tw) + sums;
+    return (nx * tx + nw * tw) / c.slots + 0.5 * std::max(tx, tw) + sums;
 }
 // (dX's 256x256 tile does not read W at any alignment: its epilogue would spill)
 inline int choose_both(int64_t M, int64_t Kp, int64_t Vc) {
-    int best = X32_W128;
-    for (int b : {X64_W128, X128_W128, X256_W256, X64_W64})
-        if ((b != X256_W256 || pack_backward(M)) && both_us(M, Kp, Vc, b) < both_us(M, Kp, Vc, best))
+    int best = X64_W64;
+    for (int b : {X32_ONCE, X64_ONCE, X64_W128, X128_W128, X256_W256})
+        if ((b > X64_ONCE || M <= 64) && (b != X256_W256 || pack_backward(M)) &&
+            both_us(M, Kp, Vc, b) < both_us(M, Kp, Vc, best))
             best = b;
     return best;
 }

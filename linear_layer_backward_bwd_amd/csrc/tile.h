@@ -528,6 +528,64 @@ __device__ __forceinline__ void accumulate(const Job &jb, int ti, int tj, LB_LDS
     ring_barrier();
 }
 
+// The same for a reduction of at most 64 indices: one pair, one slot per operand, nothing
+// to pipeline.  The small ring lets three blocks share a CU, whose loads and stores then
+// cover each other's latency.
+template <class C>
+__device__ __forceinline__ void accumulate_once(const Job &jb, int ti, int tj, LB_LDS char *smem, Acc<C> &acc) {
+    static_assert(C::S == 1 && C::SB == 1 && !C::BANY, "one pair");
+    using FA = Frags<C::TI, C::AOC, C::FI, 1>;
+    using FB = Frags<C::TJ, C::BOC, C::FJ, 1>;
+    const int lane = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Side<C::TI, C::AOC, C::kDmaA, 1> sa;
+    Side<C::TJ, C::BOC, C::kDmaB, 1> sb;
+    sa.init(jb.a, jb.lda, jb.I, jb.R, (int64_t)ti * C::TI, w, lane);
+    sb.init(jb.b, jb.ldb, jb.J, jb.R, (int64_t)tj * C::TJ, w, lane);
+    const auto xa = sa.next();
+    const auto xb = sb.next();
+#pragma unroll
+    for (int d = 0; d < C::kDmaA; ++d)
+        sa.dma(xa, smem, w, d);
+#pragma unroll
+    for (int d = 0; d < C::kDmaB; ++d)
+        sb.dma(xb, smem + C::kOffB, w, d);
+    FA fa;
+    FB fb;
+    fa.init(smem, (w / C::WJ) * C::FI * 16, lane);
+    fb.init(smem + C::kOffB, (w % C::WJ) * C::FJ * 16, lane);
+#pragma unroll
+    for (int x = 0; x < C::FI; ++x)
+#pragma unroll
+        for (int y = 0; y < C::FJ; ++y)
+            acc[x][y] = f32x4_t{};
+    vm_wait<0>();
+    ring_barrier();
+    auto half = [&](auto h) {
+        constexpr int H = decltype(h)::value;
+        u32x4_t a[C::FI], b[C::FJ];
+        frag_half_t ha[C::FI][2], hb[C::FJ][2];
+#pragma unroll
+        for (int k = 0; k < FA::kReads; ++k)
+            fa.template read<0, H>(k, 0, a, ha);
+#pragma unroll
+        for (int k = 0; k < FB::kReads; ++k)
+            fb.template read<0, H>(k, 0, b, hb);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        FA::settle(a, ha);
+        FB::settle(b, hb);
+#pragma unroll
+        for (int x = 0; x < C::FI; ++x)
+#pragma unroll
+            for (int y = 0; y < C::FJ; ++y)
+                C::T::mfma(acc[x][y], b[y], a[x]);
+    };
+    half(std::integral_constant<int, 0>{});
+    half(std::integral_constant<int, 1>{}); // zeros where R <= 32
+    mfma_drain();
+    ring_barrier();
+}
+
 // Passes a wave's sums through its own part of the ring, 16 rows at a time, so that a
 // lane holds 4 consecutive columns and 4*FJ lanes a row's FJ*16 columns (direct from the
 // accumulators a store instruction would touch 16 rows).  round(x, i, rows, j, v): v[q] is
@@ -566,10 +624,13 @@ __device__ __forceinline__ void staged(Acc<C> &acc, int64_t i0, int64_t j0, LB_L
 // begin(h) is called before round h, value(x, y) gives the 4 packed values of acc[x][y].
 // vec: rows of dst 16-byte aligned and J a multiple of 8; stores then go through a
 // descriptor of the round's rows, which drops the rows past I without a branch (with a
-// check per store each became a branch of its own).  NT: data not read again soon.
-template <class C, bool NT, class Begin, class Fn>
+// check per store each became a branch of its own).
+// nt: non-temporal stores, for data not read again soon in rows of whole 128-byte lines.
+// (Where rows start inside a line the caches have to put two waves' parts together: dW for
+// M = 15, K = 1792, V = 109976 took 285 us with non-temporal stores, 163 at V = 110080.)
+template <class C, class Begin, class Fn>
 __device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, int64_t I, int64_t J, int64_t ib,
-                                        int64_t jb, bool vec, LB_LDS char *smem, Begin begin, Fn value) {
+                                        int64_t jb, bool vec, bool nt, LB_LDS char *smem, Begin begin, Fn value) {
     constexpr int FJ = C::FJ, kRowB = FJ * 32, kChunks = 2 * FJ, kRows = 64 / kChunks;
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -603,9 +664,15 @@ __device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, 
             __builtin_amdgcn_sched_barrier(0); // all reads before the first store
             const int64_t rows = max<int64_t>(0, min<int64_t>(32, I - i0));
             const __amdgpu_buffer_rsrc_t rs = rsrc(dst + i0 * ld + jb, (uint32_t)(rows * ld * 2));
+            if (nt) {
 #pragma unroll
-            for (int q = 0; q < FJ; ++q)
-                __builtin_amdgcn_raw_buffer_store_b128(v[q], rs, (int)(off + q * step), 0, NT ? 2 : 0);
+                for (int q = 0; q < FJ; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b128(v[q], rs, (int)(off + q * step), 0, 2);
+            } else {
+#pragma unroll
+                for (int q = 0; q < FJ; ++q)
+                    __builtin_amdgcn_raw_buffer_store_b128(v[q], rs, (int)(off + q * step), 0, 0);
+            }
         } else {
             // rows of any alignment: 64 lanes store 64 neighbouring elements of a row (two
             // rows of 32), eight stores at a time
@@ -629,7 +696,7 @@ __device__ __forceinline__ void store16(Acc<C> &acc, uint16_t *dst, int64_t ld, 
                     const int r = (q0 + u) / kSegs * kPer, c = (q0 + u) % kSegs * 64;
                     const uint32_t o = (uint32_t)(lr * ld + lc + c) * 2 + (uint32_t)(r * ld * 2);
                     __builtin_amdgcn_raw_buffer_store_b16(
-                        v[u], rs, (int)(o | ((uint32_t)!(jb + c + lc < J) << 31)), 0, NT ? 2 : 0);
+                        v[u], rs, (int)(o | ((uint32_t)!(jb + c + lc < J) << 31)), 0, 0);
                 }
             }
         }

@@ -440,7 +440,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(Gr
         rp[x] = i < p.job.I ? p.row[i] : RowParam{0.0f, 0.0f, -1, 0};
     }
     const int j0 = (int)jb + 4 * (lane >> 4);
-    store16<C, false>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, smem, [](int) {}, [&](int x, int y) {
+    store16<C>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, false, smem, [](int) {}, [&](int x, int y) {
         const int t = rp[x].t < 0 ? -1 : rp[x].t - (int)p.v0;
         float g[4];
 #pragma unroll
@@ -466,7 +466,7 @@ struct BothParams {
     Job dw;            // A = X (OC), B = G (OC); J = the piece's columns
     uint16_t *dW;      // at the piece's first column
     int64_t ldw;
-    int dw_vec;
+    int dw_vec, dw_nt; // rows 16-byte aligned; of whole 128-byte lines
     const float *pow2; // [1]: factor of both outputs
     int dw_tiles;      // blocks of dW; 0: not wanted
     int dx_tiles;      // blocks of dX
@@ -530,19 +530,22 @@ __device__ __forceinline__ void dw_tile(const BothParams &p, int b, LB_LDS char 
     int ti, tj;
     coords(p.dw, gathered(b, p.dw_tiles), ti, tj);
     Acc<C> acc;
-    accumulate<C>(p.dw, ti, tj, smem, acc);
+    if constexpr (C::S == 1)
+        accumulate_once<C>(p.dw, ti, tj, smem, acc);
+    else
+        accumulate<C>(p.dw, ti, tj, smem, acc);
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
     const float f = p.pow2[1];
-    store16<C, true>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, smem, [](int) {}, [&](int x, int y) {
+    store16<C>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, p.dw_nt, smem, [](int) {}, [&](int x, int y) {
         const f32x4_t &a = acc[x][y];
         return u32x2_t{C::T::pack2(a[0] * f, a[1] * f), C::T::pack2(a[2] * f, a[3] * f)};
     });
 }
 
 template <class CX, class CW>
-__global__ __launch_bounds__(kThreads, CX::TI == 256 ? 1 : 2) void k_xent_both(BothParams p) {
+__global__ __launch_bounds__(kThreads, CX::TI == 256 ? 1 : CW::S == 1 ? 3 : 2) void k_xent_both(BothParams p) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[CX::kLds > CW::kLds ? CX::kLds : CW::kLds];
     LB_LDS char *smem = (LB_LDS char *)smem_raw;
     const int b = blockIdx.x;
@@ -591,9 +594,13 @@ __global__ __launch_bounds__(256) void k_xent_dx_sum(const float *acc, int split
 
 template <class T, int BOTH>
 struct BwdCfg;
-template <class T> struct BwdCfg<T, xent::X32_W128> {
-    using X = Cfg<T, 1, 4, 2, 2, false, false, 4>;
-    using W = Cfg<T, 2, 2, 4, 4, true, true, 2>;
+template <class T> struct BwdCfg<T, xent::X32_ONCE> {
+    using X = Cfg<T, 1, 4, 2, 2, false, false, 2>;
+    using W = Cfg<T, 1, 4, 4, 4, true, true, 1>;
+};
+template <class T> struct BwdCfg<T, xent::X64_ONCE> {
+    using X = Cfg<T, 1, 4, 4, 2, false, false, 2>;
+    using W = Cfg<T, 1, 4, 4, 4, true, true, 1>;
 };
 template <class T> struct BwdCfg<T, xent::X64_W128> {
     using X = Cfg<T, 1, 4, 4, 2, false, false, 3>;
@@ -640,7 +647,8 @@ void both_as(bool any, BothParams &p, hipStream_t s) {
 template <class T>
 void both(int which, bool any, BothParams &p, hipStream_t s) {
     switch (which) {
-    case xent::X32_W128: both_as<T, xent::X32_W128>(any, p, s); break;
+    case xent::X32_ONCE: both_as<T, xent::X32_ONCE>(any, p, s); break;
+    case xent::X64_ONCE: both_as<T, xent::X64_ONCE>(any, p, s); break;
     case xent::X64_W128: both_as<T, xent::X64_W128>(any, p, s); break;
     case xent::X128_W128: both_as<T, xent::X128_W128>(any, p, s); break;
     case xent::X256_W256: // never with `any`
@@ -711,6 +719,7 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
         p.dW = a.dW ? static_cast<uint16_t *>(a.dW) + v0 : nullptr;
         p.ldw = a.V;
         p.dw_vec = a.V % 8 == 0 && aligned(a.dW, 16);
+        p.dw_nt = a.V % 64 == 0 && aligned(a.dW, 128);
         p.pow2 = pow2;
         p.want_dx = a.dX != nullptr;
         grad<T>(b.rows, ragged && !pack_w, g, s);

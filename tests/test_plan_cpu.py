@@ -12,8 +12,8 @@ import pytest
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "linear_layer_backward_bwd_amd", "csrc")
-TILE = {0: (32, 128), 1: (64, 128), 2: (128, 128), 3: (256, 256), 4: (64, 64)}
-BOTH = {0: (0, 2), 1: (1, 2), 2: (2, 2), 3: (3, 3), 4: (4, 4)}
+TILE = {0: (32, 128), 1: (64, 128), 2: (128, 128), 3: (256, 256), 4: (64, 64), 5: (64, 256)}
+BOTH = {0: (0, 5), 1: (1, 5), 2: (2, 2), 3: (3, 3), 4: (4, 4), 5: (1, 2)}
 
 
 @pytest.fixture(scope="module")
@@ -94,6 +94,8 @@ def test_backward_plan(probe, pack):
             assert total <= b[1]
         if M <= 256:                              # these tiles read W at any alignment
             assert both != 3
+        if both in (0, 1):                        # dW's whole reduction at once
+            assert M <= 64
         assert 2 * M * Vc <= (512 << 20) or Vc == 256
         (xi, xj), (wi, wj) = TILE[BOTH[both][0]], TILE[BOTH[both][1]]
         blocks = splits * -(-M // xi) * -(-Kp // xj) + -(-K // wi) * -(-Vc // wj)
