@@ -307,80 +307,111 @@ __device__ __forceinline__ void store_small(const ProductParams &p, const Job &j
         });
 }
 
-// The last product, on the caller's matrices.  VEC: their rows take 4 elements at a time.
+// The last product, on the caller's matrices.  VEC: their rows take 4 elements at a time;
+// what a round combines with (X, and W of UPDATE) is then loaded a round ahead through
+// descriptors of the round's 16 rows, which drop the rows past I.
 template <class C, int STEP, bool VEC>
 __device__ __forceinline__ void store_last(const ProductParams &p, const Job &job, int64_t b, int ti, int tj,
                                            LB_LDS char *smem) {
     Acc<C> acc;
     accumulate<C>(job, ti, tj, smem, acc);
+    constexpr int kChunks = 4 * C::FJ;
+    const int lane = threadIdx.x & 63;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
-    const int64_t I = job.I, J = job.J;
-    const uint16_t *const add = p.add + b * p.step_add; // ld a multiple of 8, padded
-    const int64_t mine = b * I * J;
-    u32x2_t x[C::FJ];
-    f32x4_t w[C::FJ];
-    auto load = [&](int64_t i, int rows, int64_t j) {
-#pragma unroll
-        for (int q = 0; q < C::FJ; ++q) {
-            const int64_t r = i + q * rows;
-            const bool in = r < I && j < J;
-            x[q] = in ? *reinterpret_cast<const u32x2_t *>(add + r * p.ld_add + j) : u32x2_t{};
-            if constexpr (STEP == UPDATE && VEC)
-                w[q] = in ? *reinterpret_cast<const f32x4_t *>(p.W + mine + r * J + j) : f32x4_t{};
-        }
+    const int64_t I = job.I, J = job.J, mine = b * I * J;
+    const int64_t iw = i0 + (wv / C::WJ) * C::FI * 16, jw = j0 + (wv % C::WJ) * C::FJ * 16; // the wave's corner
+    const uint16_t *const add = p.add + b * p.step_add;
+    const int lr = lane / kChunks, lc = 4 * (lane % kChunks);
+    const uint32_t skip = (uint32_t)!(jw + lc < J) << 31;
+    const uint32_t off_x = (uint32_t)(lr * p.ld_add + lc) * 2 | skip, off_w = (uint32_t)(lr * J + lc) * 4 | skip;
+    // bytes of the round's rows from the wave's first column on
+    auto window = [&](int k, int64_t ld, int bytes) {
+        const int64_t rows = max<int64_t>(0, min<int64_t>(16, I - (iw + 16 * k)));
+        return rows && jw < J ? (uint32_t)(((rows - 1) * ld + J - jw) * bytes) : 0u;
     };
-    staged<C>(
-        acc, i0, j0, smem,
-        [&](int, int64_t i, int rows, int64_t j) {
-            load(i, rows, j);
-        },
-        [&](int, int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
+    u32x2_t x[2][C::FJ];
+    f32x4_t w[2][C::FJ];
+    auto load = [&](int k, int rows) {
+        if constexpr (VEC) {
+            const int64_t i = iw + 16 * k;
+            const __amdgpu_buffer_rsrc_t rx = rsrc(add + i * p.ld_add + jw, window(k, p.ld_add, 2));
+            const __amdgpu_buffer_rsrc_t rw =
+                rsrc(STEP == UPDATE ? p.W + mine + i * J + jw : nullptr, STEP == UPDATE ? window(k, J, 4) : 0u);
 #pragma unroll
             for (int q = 0; q < C::FJ; ++q) {
-                const int64_t r = i + q * rows;
-                if (r >= I || j >= J)
-                    continue;
-                const f32x4_t a = f16x4(x[q]);
-                f32x4_t t;
+                x[k & 1][q] = __builtin_bit_cast(
+                    u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(
+                                 rx, (int)(off_x + (uint32_t)(q * rows * p.ld_add * 2)), 0, 0));
+                if constexpr (STEP == UPDATE)
+                    w[k & 1][q] = __builtin_bit_cast(
+                        f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                     rw, (int)(off_w + (uint32_t)(q * rows * J * 4)), 0, 0));
+            }
+        }
+    };
+    auto stepped = [&](float old, float o) { return old - p.lr * (p.scale * o + p.wd * old); };
+    staged<C>(
+        acc, i0, j0, smem,
+        [&](int k, int64_t, int rows, int64_t) {
+            if (k == 0)
+                load(0, rows);
+            if (k + 1 < C::FI)
+                load(k + 1, rows);
+        },
+        [&](int k, int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
+            if constexpr (VEC) {
+                const int64_t r0 = iw + 16 * k;
+                const __amdgpu_buffer_rsrc_t ro = rsrc(STEP == ORTH ? p.o + mine + r0 * J + jw : nullptr,
+                                                       STEP == ORTH ? window(k, J, 2) : 0u);
+                const __amdgpu_buffer_rsrc_t rw = rsrc(STEP == UPDATE ? p.W + mine + r0 * J + jw : nullptr,
+                                                       STEP == UPDATE ? window(k, J, 4) : 0u);
+                const bool copy = STEP == UPDATE && p.W16;
+                const __amdgpu_buffer_rsrc_t rc =
+                    rsrc(copy ? p.W16 + mine + r0 * J + jw : nullptr, copy ? window(k, J, 2) : 0u);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    t[e] = __builtin_fmaf(p.fa, a[e], p.f * v[q][e]);
-                const int64_t at = mine + r * J + j;
-                if constexpr (STEP == ORTH) {
-                    uint16_t h[4];
+                for (int q = 0; q < C::FJ; ++q) {
+                    const f32x4_t a = f16x4(x[k & 1][q]);
+                    f32x4_t t;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        h[e] = p.o_bf16 ? BF16::one(t[e]) : F16::one(t[e]);
-                    if constexpr (VEC) {
-                        *reinterpret_cast<u32x2_t *>(p.o + at) =
-                            u32x2_t{(uint32_t)h[0] | ((uint32_t)h[1] << 16), (uint32_t)h[2] | ((uint32_t)h[3] << 16)};
-                    } else {
+                        t[e] = __builtin_fmaf(p.fa, a[e], p.f * v[q][e]);
+                    const uint32_t o4 = off_w + (uint32_t)(q * rows * J * 4);
+                    const uint32_t o2 = (uint32_t)((lr + q * rows) * J + lc) * 2 | skip;
+                    if constexpr (STEP == UPDATE) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            if (j + e < J)
-                                p.o[at + e] = h[e];
+                            t[e] = stepped(w[k & 1][q][e], t[e]);
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, t), rw, (int)o4, 0, 0);
                     }
-                } else {
-                    auto stepped = [&](float old, float o) { return old - p.lr * (p.scale * o + p.wd * old); };
-                    if constexpr (VEC) {
-                        f32x4_t n;
+                    const u32x2_t h = p.o_bf16 ? u32x2_t{BF16::pack2(t[0], t[1]), BF16::pack2(t[2], t[3])}
+                                               : u32x2_t{F16::pack2(t[0], t[1]), F16::pack2(t[2], t[3])};
+                    if constexpr (STEP == ORTH)
+                        __builtin_amdgcn_raw_buffer_store_b64(h, ro, (int)o2, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b64(h, rc, (int)o2, 0, 0); // dropped without a copy
+                }
+            } else {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            n[e] = stepped(w[q][e], t[e]);
-                        *reinterpret_cast<f32x4_t *>(p.W + at) = n;
-                        if (p.W16)
-                            *reinterpret_cast<u32x2_t *>(p.W16 + at) =
-                                p.o_bf16 ? u32x2_t{BF16::pack2(n[0], n[1]), BF16::pack2(n[2], n[3])}
-                                         : u32x2_t{F16::pack2(n[0], n[1]), F16::pack2(n[2], n[3])};
-                    } else {
+                for (int q = 0; q < C::FJ; ++q) {
+                    const int64_t r = i + q * rows;
+                    if (r >= I || j >= J)
+                        continue;
+                    const f32x4_t a = f16x4(*reinterpret_cast<const u32x2_t *>(add + r * p.ld_add + j));
+                    const int64_t at = mine + r * J + j;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (j + e < J) {
-                                const float n = stepped(p.W[at + e], t[e]);
-                                p.W[at + e] = n;
-                                if (p.W16)
-                                    p.W16[at + e] = p.o_bf16 ? BF16::one(n) : F16::one(n);
-                            }
+                    for (int e = 0; e < 4; ++e) {
+                        const float t = __builtin_fmaf(p.fa, a[e], p.f * v[q][e]);
+                        if (j + e >= J)
+                            continue;
+                        if constexpr (STEP == ORTH) {
+                            p.o[at + e] = p.o_bf16 ? BF16::one(t) : F16::one(t);
+                        } else {
+                            const float n = stepped(p.W[at + e], t);
+                            p.W[at + e] = n;
+                            if (p.W16)
+                                p.W16[at + e] = p.o_bf16 ? BF16::one(n) : F16::one(n);
+                        }
                     }
                 }
             }

@@ -514,7 +514,7 @@ __device__ __forceinline__ void dx_tile(const BothParams &p, int b, LB_LDS char 
                 *reinterpret_cast<f32x4_t *>(part + r * p.Kp + j) = v[q];
             } else if (p.dx_vec && j < K) {
                 const u32x2_t h = {C::T::pack2(v[q][0] * f, v[q][1] * f), C::T::pack2(v[q][2] * f, v[q][3] * f)};
-                __builtin_nontemporal_store(h, reinterpret_cast<u32x2_t *>(p.dX + r * K + j));
+                *reinterpret_cast<u32x2_t *>(p.dX + r * K + j) = h;
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)

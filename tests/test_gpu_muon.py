@@ -147,6 +147,17 @@ def test_batch_is_the_matrices_one_by_one():
         assert torch.equal(whole[i], lb.muon_orth(G[i]))
 
 
+def test_batch_past_2_to_31_elements():
+    """700 matrices of 1760 x 1760, each the one of a few repeated ones that it should be."""
+    few = gradient((4, 1760, 1760), 70).to(DEV, torch.bfloat16)
+    G = few.repeat(175, 1, 1)
+    out = lb.muon_orth(G)
+    want = lb.muon_orth(few)
+    check_orth(want[:1], few[:1], H[want.dtype])
+    for i in (0, 1, 2, 3, 346, 347, 693, 694, 695, 699):
+        assert torch.equal(out[i], want[i % 4])
+
+
 def test_empty():
     for shape in ((0, 8, 8), (2, 0, 8), (2, 8, 0)):
         G = torch.empty(shape, device=DEV)

@@ -363,3 +363,52 @@ def test_two_streams_at_once():
     for a, b in zip(want, got):
         for x, y in zip(a, b):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("M,K,V", [(200001, 16, 40), (70000, 9, 130)])
+def test_many_rows(M, K, V):
+    X, W, t = case(M, K, V, "bf16", seed=40)
+    loss, lse, out, dX, dW = both(X, W, t, "bf16")
+    check_forward(X, W, t, (loss, lse, out))
+    check_backward(X, W, t, lse, dX, dW, "bf16")
+
+
+@pytest.mark.parametrize("M,V", [(3, 1 << 21), (3, (1 << 21) + 5), (300, 1 << 21)])
+def test_weights_past_4_gib(M, V):
+    """W and dW of 4.6 GB: every row of the loss and of dX, dW on sampled rows."""
+    K = 1100
+    g = torch.Generator(device=DEV).manual_seed(41)
+    X = torch.randn(M, K, device=DEV, generator=g).bfloat16()
+    W = torch.empty(K, V, dtype=torch.bfloat16, device=DEV).normal_(0, 0.03, generator=g)
+    t = torch.randint(0, V, (M,), device=DEV, generator=g)
+    t[0], t[1] = V - 1, -1
+    loss, lse, out = lb.lin_xent(X, W, t)
+    dX, dW = torch.full_like(X, float("nan")), torch.full_like(W, float("nan"))
+    lb.lin_xent_bwd(X, W, t, lse, dX, dW)
+    z = torch.cat([X.double() @ W[:, lo:lo + (1 << 18)].double() for lo in range(0, V, 1 << 18)], 1)
+    keep = t >= 0
+    rl = torch.where(keep, torch.logsumexp(z, 1), 0.0)
+    ro = torch.where(keep, rl - z.gather(1, t.clamp(min=0)[:, None])[:, 0], 0.0)
+    # |dz| <= gamma(K) sum |x w| < 2^-24 * 99 * K * 0.06 and the statistics of 2^21 columns
+    bound = 99 * U * K * 0.06 + U * (90 + 26 * (V / 512 + 16)) + 4 * U * 16
+    assert float((lse.double() - rl).abs().max()) <= bound and float((loss.double() - ro).abs().max()) <= 2 * bound
+    G = torch.exp(z - rl[:, None])
+    G.scatter_add_(1, t.clamp(min=0)[:, None], -torch.ones_like(G[:, :1]))
+    G *= keep[:, None]
+    ref = sum(G[:, lo:lo + (1 << 18)] @ W[:, lo:lo + (1 << 18)].double().T.contiguous() for lo in range(0, V, 1 << 18))
+    # the roundings of G and of dX, each at most half a bf16 step of its terms
+    assert float((dX.double() - ref).norm()) <= 2 * H["bf16"] * float(ref.norm())
+    rows = torch.tensor([0, 1, 511, 1023, K - 1], device=DEV)
+    ref = X[:, rows].double().T @ G
+    assert float((dW[rows].double() - ref).norm()) <= 2 * H["bf16"] * float(ref.norm())
+    assert bool(dW[rows].isfinite().all())
+
+
+def test_strided_views_are_refused():
+    X, W, t = case(8, 64, 128, "bf16", seed=42)
+    with pytest.raises(ValueError):
+        lb.lin_xent(X[:, :32], W[:32], t)
+    with pytest.raises(ValueError):
+        lb.lin_xent(X, W[:, ::2], t)
+    with pytest.raises(ValueError):
+        lb.lin_xent(X, W, t, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
