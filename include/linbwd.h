@@ -314,9 +314,9 @@ int lin_xent(const void *X, const void *W, const int64_t *target, float *loss, f
  * Rows with a negative target, or with s[m] = 0, have no gradient: their dX is 0
  * and their X is not used, whatever it holds.  A target >= V makes its row's dX
  * and all of dW NaN.  G is rounded once to dtype, the operand type of the two
- * products (for LB_F16 after scaling by the power of two that brings max |s| to
- * [2^14, 2^15), so small probabilities stay above fp16's smallest normal; taken
- * out in fp32), dX and dW once at the end.  Results repeat bit for bit.
+ * products, in units of max |s| (fp16: of 2^-14 of that, so small probabilities
+ * stay above its smallest normal) that the fp32 sums are multiplied by; dX and dW
+ * are rounded once at the end.  Results repeat bit for bit.
  * M = 0 fills dW with zeros.  Both outputs NULL is a no-op.  Errors: lin_xent's.
  */
 int64_t lin_xent_bwd_workspace(int64_t M, int64_t K, int64_t V);

@@ -18,9 +18,11 @@
 //
 // Rounding: products of 16-bit operands accumulate in fp32; statistics, lse and the
 // sums of dX over pieces are fp32, the mean is summed in fp64; G is rounded once to
-// the operands' type, dX and dW once at the end.  For fp16, G is scaled by a power of
-// two that brings max |s| to [2^14, 2^15), so that the probabilities of a large
-// vocabulary stay above fp16's smallest normal; the epilogues take it out again.
+// the operands' type, dX and dW once at the end.  G is made with s / max |s|, and the
+// epilogues multiply by max |s| in fp32: with s itself every entry −s of the targets
+// would be off by the same rounding of s, a bias of the whole gradient by up to half a
+// step (dW 3.1e-3 off against 2.3e-3).  For fp16 it is scaled up by 2^14 besides, so
+// that the probabilities of a large vocabulary stay above fp16's smallest normal.
 #include "kernels.h"
 #include "plan_xent.h"
 #include "tile.h"
@@ -43,7 +45,7 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 // What the backward pass needs of a row.
 struct RowParam {
     float lse2; // lse·log2(e)
-    float s;    // upstream gradient · power of two
+    float s;    // upstream gradient over the factor of the outputs
     int t;      // target, -1: none
     int pad;
 };
@@ -352,8 +354,8 @@ bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n
 
 // ---- backward --------------------------------------------------------------------------
 // Row parameters, by the first block, and X's copy (rows that take no part as zeros: theirs
-// may hold anything), by the others.  fp16: the power of two that brings max |s| to
-// [2^14, 2^15); bf16 has fp32's range and takes 1.  pow2[0], pow2[1]: it and its inverse.
+// may hold anything), by the others.  factor[0] is what both outputs are multiplied by:
+// max |s| (or 1 if that is 0, infinite or NaN), over 2^14 for fp16.
 struct PrepParams {
     const int64_t *target;
     const float *lse, *row_scale, *d_scale;
@@ -361,7 +363,7 @@ struct PrepParams {
     int64_t M, K, V, Kp;
     int f16;
     RowParam *row;
-    float *pow2;
+    float *factor;
     const uint16_t *X;
     uint16_t *x;
 };
@@ -375,31 +377,22 @@ __global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
                   (int64_t)(gridDim.x - 1) * 256, [&](int64_t r) { return p.target[r] >= 0 && s_of(r) != 0.0f; });
         return;
     }
-    float f = 1.0f;
-    if (p.f16) {
-        float mx = 0.0f;
+    float mx = 0.0f;
 #pragma unroll 4
-        for (int64_t i = threadIdx.x; i < p.M; i += 256)
-            if (p.target[i] >= 0)
-                mx = fmaxf(mx, fabsf(s_of(i)));
-        sh[threadIdx.x] = mx;
+    for (int64_t i = threadIdx.x; i < p.M; i += 256)
+        if (p.target[i] >= 0)
+            mx = fmaxf(mx, fabsf(s_of(i)));
+    sh[threadIdx.x] = mx;
+    __syncthreads();
+    for (int h = 128; h > 0; h >>= 1) {
+        if ((int)threadIdx.x < h)
+            sh[threadIdx.x] = fmaxf(sh[threadIdx.x], sh[threadIdx.x + h]);
         __syncthreads();
-        for (int h = 128; h > 0; h >>= 1) {
-            if ((int)threadIdx.x < h)
-                sh[threadIdx.x] = fmaxf(sh[threadIdx.x], sh[threadIdx.x + h]);
-            __syncthreads();
-        }
-        mx = sh[0];
-        if (mx > 0.0f && mx < INFINITY) {
-            int e;
-            (void)frexpf(mx, &e); // mx in [2^(e-1), 2^e)
-            f = ldexpf(1.0f, max(-100, min(100, 15 - e)));
-        }
     }
-    if (threadIdx.x == 0) {
-        p.pow2[0] = f;
-        p.pow2[1] = 1.0f / f;
-    }
+    const float unit = p.f16 ? 16384.0f : 1.0f;
+    mx = sh[0] > 0.0f && sh[0] < INFINITY ? sh[0] : 1.0f;
+    if (threadIdx.x == 0)
+        p.factor[0] = mx / unit;
 #pragma unroll 4
     for (int64_t i = threadIdx.x; i < p.M; i += 256) {
         const int64_t t = p.target[i];
@@ -408,7 +401,7 @@ __global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
         if (t >= p.V)
             r = RowParam{0.0f, NAN, -1, 0}; // no such class: the gradients say so
         else if (t >= 0 && s != 0.0f)
-            r = RowParam{p.lse[i] * kLog2e, s * f, (int)t, 0};
+            r = RowParam{p.lse[i] * kLog2e, s / mx * unit, (int)t, 0};
         p.row[i] = r;
     }
 }
@@ -467,7 +460,7 @@ struct BothParams {
     uint16_t *dW;      // at the piece's first column
     int64_t ldw;
     int dw_vec, dw_nt; // rows 16-byte aligned; of whole 128-byte lines
-    const float *pow2; // [1]: factor of both outputs
+    const float *factor; // of both outputs
     int dw_tiles;      // blocks of dW; 0: not wanted
     int dx_tiles;      // blocks of dX
     int dx_first;      // the longer tiles are launched first
@@ -491,7 +484,7 @@ __device__ __forceinline__ void dx_tile(const BothParams &p, int b, LB_LDS char 
     const int64_t i0 = (int64_t)ti * C::TI, j0 = (int64_t)tj * C::TJ;
     const int64_t M = j.I, K = j.J;
     float *const part = p.acc ? p.acc + (int64_t)sp * M * p.Kp : nullptr;
-    const float f = p.pow2[1];
+    const float f = p.factor[0];
     const bool out = p.splits == 1 && p.last;
     staged<C>(acc, i0, j0, smem, [](int, int64_t, int, int64_t) {}, [&](int, int64_t i, int rows, int64_t j, f32x4_t (&v)[C::FJ]) {
         if (!p.first) {
@@ -537,7 +530,7 @@ __device__ __forceinline__ void dw_tile(const BothParams &p, int b, LB_LDS char 
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
-    const float f = p.pow2[1];
+    const float f = p.factor[0];
     store16<C>(acc, p.dW, p.ldw, p.dw.I, p.dw.J, ib, jb, p.dw_vec, p.dw_nt, smem, [](int) {}, [&](int x, int y) {
         const f32x4_t &a = acc[x][y];
         return u32x2_t{C::T::pack2(a[0] * f, a[1] * f), C::T::pack2(a[2] * f, a[3] * f)};
@@ -560,10 +553,10 @@ __global__ __launch_bounds__(kThreads, CX::TI == 256 ? 1 : CW::S == 1 ? 3 : 2) v
 // quarter of the ranges (in turn), the four sums added in wave order.
 template <class T>
 __global__ __launch_bounds__(256) void k_xent_dx_sum(const float *acc, int splits, int64_t M, int64_t K, int64_t Kp,
-                                                     const float *pow2, uint16_t *dX, int vec) {
+                                                     const float *factor, uint16_t *dX, int vec) {
     __shared__ f32x4_t sh[4][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const float f = pow2[1];
+    const float f = factor[0];
     const int64_t n = M * Kp / 4;
     for (int64_t q0 = (int64_t)blockIdx.x * 64; q0 < n; q0 += (int64_t)gridDim.x * 64) {
         const int64_t q = q0 + lane;
@@ -664,10 +657,10 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
     const xent::Bwd b = xent::backward(a.M, a.K, a.V, pack_w);
     char *const ws = static_cast<char *>(a.ws);
     RowParam *const row = reinterpret_cast<RowParam *>(ws + b.off_row);
-    float *const pow2 = reinterpret_cast<float *>(ws + b.off_row + 16 * a.M);
+    float *const factor = reinterpret_cast<float *>(ws + b.off_row + 16 * a.M);
     uint16_t *const x = reinterpret_cast<uint16_t *>(ws + b.off_x);
     uint16_t *const wp = reinterpret_cast<uint16_t *>(ws + b.off_w);
-    PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16, row, pow2,
+    PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16, row, factor,
                   static_cast<const uint16_t *>(a.X), x};
     const int64_t copies = std::min<int64_t>(cdiv(a.M * (b.Kp / 8), 256), 8 * xent::kCUs);
     hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(1 + copies)), dim3(256), 0, s, pp);
@@ -720,7 +713,7 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
         p.ldw = a.V;
         p.dw_vec = a.V % 8 == 0 && aligned(a.dW, 16);
         p.dw_nt = a.V % 64 == 0 && aligned(a.dW, 128);
-        p.pow2 = pow2;
+        p.factor = factor;
         p.want_dx = a.dX != nullptr;
         grad<T>(b.rows, ragged && !pack_w, g, s);
         both<T>(b.both, ragged && !pack_w, p, s);
@@ -728,7 +721,7 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
     if (a.dX && b.splits > 1) {
         const int64_t blocks = std::min<int64_t>(cdiv(a.M * b.Kp / 4, 64), 32 * xent::kCUs);
         hipLaunchKernelGGL((k_xent_dx_sum<T>), dim3((unsigned)blocks), dim3(256), 0, s,
-                           reinterpret_cast<const float *>(ws + b.off_acc), b.splits, a.M, a.K, b.Kp, pow2,
+                           reinterpret_cast<const float *>(ws + b.off_acc), b.splits, a.M, a.K, b.Kp, factor,
                            static_cast<uint16_t *>(a.dX), (int)dx_vec);
     }
     return hipGetLastError();

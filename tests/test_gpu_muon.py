@@ -170,6 +170,17 @@ def test_repeatable_bit_for_bit(shape):
     assert torch.equal(lb.muon_orth(G), lb.muon_orth(G))
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 5, 3), (3, 130, 70), (1, 60, 4000), (2, 300, 1001), (1, 4000, 100),
+                                   (5, 257, 129)])
+def test_workspace_of_exactly_the_size_asked_for(shape):
+    G = gradient(shape, 80).to(DEV)
+    need = lb.muon_workspace(*shape)
+    whole = torch.full((need + 8192,), 90, dtype=torch.uint8, device=DEV)
+    out = lb.muon_orth(G, ws=whole[4096:4096 + need])
+    assert torch.equal(out, lb.muon_orth(G))
+    assert bool((whole[:4096] == 90).all()) and bool((whole[4096 + need:] == 90).all())
+
+
 # ---- the update ------------------------------------------------------------------------
 LR, BETA, WD = 3e-4, 0.95, 0.1
 

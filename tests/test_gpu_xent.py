@@ -412,3 +412,25 @@ def test_strided_views_are_refused():
         lb.lin_xent(X, W[:, ::2], t)
     with pytest.raises(ValueError):
         lb.lin_xent(X, W, t, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 3, 5), (17, 65, 1001), (33, 64, 256), (65, 130, 777), (200, 72, 520),
+                                   (300, 100, 1025), (2600, 40, 333), (4097, 24, 200)])
+@pytest.mark.parametrize("offset", [0, 1])
+def test_workspace_of_exactly_the_size_asked_for(M, K, V, offset):
+    X, W, t = case(M, K, V, "bf16", seed=50, offset=offset)
+    loss, lse, out = lb.lin_xent(X, W, t)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    lb.lin_xent_bwd(X, W, t, lse, dX, dW)
+    for need in (lb.lin_xent_workspace(M, K, V), lb.lin_xent_bwd_workspace(M, K, V)):
+        whole = torch.full((need + 8192,), 90, dtype=torch.uint8, device=DEV)
+        ws = whole[4096:4096 + need]
+        if need == lb.lin_xent_workspace(M, K, V):
+            got = lb.lin_xent(X, W, t, ws=ws)
+            for a, b in zip(got, (loss, lse, out)):
+                assert torch.equal(a, b)
+        if need == lb.lin_xent_bwd_workspace(M, K, V):
+            gX, gW = torch.empty_like(X), torch.empty_like(W)
+            lb.lin_xent_bwd(X, W, t, lse, gX, gW, ws=ws)
+            assert torch.equal(gX, dX) and torch.equal(gW, dW)
+        assert bool((whole[:4096] == 90).all()) and bool((whole[4096 + need:] == 90).all())
