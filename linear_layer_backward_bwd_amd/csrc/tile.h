@@ -27,8 +27,13 @@
 // issued too, through an empty buffer descriptor (they read zero), so the loop has
 // no tail: only one wait count and one branch.
 //
-// Bound: MFMA for the 256x256 tile (8x8 fragments per wave: 16-24 KiB of LDS reads
-// per 64 MFMAs); the smaller tiles serve short sides, where HBM bounds the call.
+// Bound.  256x256 (8x8 fragments per wave, 256 LDS bytes per MFMA): MFMA and the power
+// limit; 1.36-1.42 PFLOP/s over whole calls, matrix pipes 66-73% busy at 1.7-1.9 GHz.  B has
+// three slots there, A two (160 KiB of LDS): B's DMA, issued after A's, gets a pair more to
+// land (Muon's A at 4096 x 4096 over 12288: 272 -> 256 us).  128x128 (512 LDS bytes per MFMA):
+// LDS, 1536 cycles of reads and DMA for 1024 of MFMA with two blocks on a CU; it fills the
+// card where there are few tiles.  64x64 and the 32- and 64-row tiles: latency (0.25 us a
+// pair) or HBM.
 #pragma once
 
 #include "device.h"
