@@ -284,7 +284,9 @@ int softmax_bwd(const void *P, const void *dY, void *dX, int64_t rows, int64_t c
  *           may overlap (other streams, two graphs) take workspaces of their own.
  *
  * Any alignment of the elements and any K and V from 1 to 2^22 − 1; M < 2^27.
- * M = 0 writes out = 0, 0 only.  NaN and infinity propagate to their rows.
+ * M = 0 writes out = 0, 0 only.  NaN and infinity propagate to their rows.  A loss
+ * near 0 (a row that is nearly sure) keeps its digits however large the logits are:
+ * it is taken from the sum of exponentials, not as lse − z.
  * Errors: LB_EDTYPE for another dtype (fp32 operands have no MFMA path here);
  * LB_EINVAL for a size out of range, a NULL buffer, or a workspace that is NULL,
  * unaligned or too small; LB_EHIP when a launch fails.

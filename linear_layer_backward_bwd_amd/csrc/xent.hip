@@ -273,8 +273,12 @@ __global__ __launch_bounds__(1024) void k_xent_join(JoinParams p) {
         p.run[i] = a;
         if (p.last) {
             const int64_t t = p.target[i];
-            const float lse = (a.x + __builtin_log2f(a.y)) * kLn2;
-            const float loss = t < 0 ? 0.0f : t < p.V ? lse - p.zt[i] : NAN;
+            // the loss from the logarithm's two parts, the target's exponent as it is in the sum:
+            // lse − z has lost half a step of |z|, all of the loss of a row that is nearly sure
+            const float log2s = __builtin_log2f(a.y);
+            const float lse = (a.x + log2s) * kLn2;
+            const float own = t < 0 || t >= p.V ? 0.0f : __builtin_fmaf(p.zt[i], kLog2e, -a.x);
+            const float loss = t < 0 ? 0.0f : t < p.V ? (log2s - own) * kLn2 : NAN;
             p.lse[i] = t < 0 ? 0.0f : lse;
             p.loss[i] = loss;
             s = Sum{(double)loss, t >= 0};

@@ -434,3 +434,24 @@ def test_workspace_of_exactly_the_size_asked_for(M, K, V, offset):
             lb.lin_xent_bwd(X, W, t, lse, gX, gW, ws=ws)
             assert torch.equal(gX, dX) and torch.equal(gW, dW)
         assert bool((whole[:4096] == 90).all()) and bool((whole[4096 + need:] == 90).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("M,V", [(1, 40), (70, 1000), (300, 3001)])
+def test_loss_of_a_nearly_sure_row(M, V, dtype):
+    """Exact logits: 1000 for the target, 984 for the others, so loss = log1p((V − 1) e^-16).  The
+    sum is 2^d (1 + (V − 1) e^-16), where d is what rounding the maximum's exponent left (up to
+    2^-14) and cancels: 2^d and the logarithm are off by a few u, and each of up to 128 additions
+    beside the 1 by u (lse − z is off by 1000 u)."""
+    X = torch.zeros(M, 8, dtype=T[dtype], device=DEV)
+    X[:, 3] = 1.0
+    W = torch.full((8, V), 984.0, dtype=T[dtype], device=DEV)
+    hit = V // 3
+    W[:, hit] = 1000.0
+    t = torch.full((M,), hit, dtype=torch.int64, device=DEV)
+    loss, lse, out = lb.lin_xent(X, W, t)
+    ref = float(np.log1p((V - 1) * np.exp(-16.0)))
+    bound = (128 + 32) * U
+    assert bool(((loss.double() - ref).abs() <= bound).all()), float((loss.double() - ref).abs().max())
+    assert abs(out[0].item() - ref) <= bound
+    assert bool(((lse.double() - 1000.0 - ref).abs() <= 4 * U * 1000 + bound).all())
