@@ -181,6 +181,16 @@ def test_workspace_of_exactly_the_size_asked_for(shape):
     assert bool((whole[:4096] == 90).all()) and bool((whole[4096 + need:] == 90).all())
 
 
+@pytest.mark.parametrize("shape", [(1, 1, 1), (2, 5, 3), (3, 130, 70), (1, 60, 4000), (2, 300, 1001), (1, 4000, 100),
+                                   (5, 257, 129), (2, 515, 523), (1, 1100, 1301)])
+def test_a_workspace_full_of_nan(shape):
+    """What a workspace held before the call reaches nothing."""
+    G = gradient(shape, 81).to(DEV)
+    got = [lb.muon_orth(G, ws=torch.full((lb.muon_workspace(*shape),), fill, dtype=torch.uint8, device=DEV))
+           for fill in (0, 255)]
+    assert torch.equal(*got) and not bool(got[0].isnan().any())
+
+
 # ---- the update ------------------------------------------------------------------------
 LR, BETA, WD = 3e-4, 0.95, 0.1
 

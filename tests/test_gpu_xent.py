@@ -455,3 +455,37 @@ def test_loss_of_a_nearly_sure_row(M, V, dtype):
     assert bool(((loss.double() - ref).abs() <= bound).all()), float((loss.double() - ref).abs().max())
     assert abs(out[0].item() - ref) <= bound
     assert bool(((lse.double() - 1000.0 - ref).abs() <= 4 * U * 1000 + bound).all())
+
+
+@pytest.mark.parametrize("M", [900, 5000])
+def test_row_weights_of_many_rows(M):
+    """The largest |s| from the rows themselves and from a launch of its own; weights of rows out
+    of the loss may hold anything."""
+    X, W, t = case(M, 40, 300, "f16", seed=9)
+    w = torch.rand(M, device=DEV) * 2e-5
+    big = int(((t >= 0).nonzero())[-1])
+    w[big] = -3.0
+    lse = lb.lin_xent(X, W, t)[1]
+    poison = torch.where(t < 0, torch.tensor(float("nan"), device=DEV), w)
+    poison[int((t < 0).nonzero()[0])] = float("inf")
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    lb.lin_xent_bwd(X, W, t, lse, dX, dW, scale=64.0, row_scale=poison)
+    check_backward(X, W, t, lse, dX, dW, "f16", 64.0, None, torch.where(t < 0, torch.zeros_like(w), w))
+
+
+@pytest.mark.parametrize("M,K,V", [(1, 3, 5), (17, 65, 1001), (33, 64, 256), (65, 130, 777), (200, 72, 520),
+                                   (300, 100, 1025), (2600, 40, 333), (600, 24, 20011)])
+def test_a_workspace_full_of_nan(M, K, V):
+    """What a workspace held before the call reaches nothing."""
+    X, W, t = case(M, K, V, "bf16", seed=51)
+    got = []
+    for fill in (0, 255):
+        ws = torch.full((max(lb.lin_xent_workspace(M, K, V), lb.lin_xent_bwd_workspace(M, K, V)),), fill,
+                        dtype=torch.uint8, device=DEV)
+        loss, lse, out = lb.lin_xent(X, W, t, ws=ws)
+        ws.fill_(fill)
+        dX, dW = torch.empty_like(X), torch.empty_like(W)
+        lb.lin_xent_bwd(X, W, t, lse, dX, dW, ws=ws)
+        got.append((loss, lse, out, dX, dW))
+    for a, b in zip(*got):
+        assert torch.equal(a, b) and not bool(a.isnan().any())
