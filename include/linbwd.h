@@ -8,7 +8,7 @@
  * master copy of the weights with AdamW.
  *
  * Around that path it has the softmax cross entropy of the model's head, where
- * the backward pass starts.
+ * the backward pass starts, and Muon, the update of weight matrices beside AdamW.
  *
  * Conventions for every entry point:
  *  - All tensor pointers are DEVICE pointers on the current HIP device,

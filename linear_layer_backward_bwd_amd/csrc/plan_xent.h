@@ -30,7 +30,6 @@ inline Shape shape(int r) {
     case ROWS256: return {256, 256, kCUs, 11.0, 1.03, 1.03};
     case SQUARE64: return {64, 64, 2 * kCUs, 2.8, 0.24, 0.34};
     default: return {64, 256, 3 * kCUs, 5.0, 0.30, 0.60}; // a reduction of at most 64
-
     }
 }
 inline int64_t tiles(int r, int64_t I, int64_t J) { return cdiv(I, shape(r).ti) * cdiv(J, shape(r).tj); }
@@ -66,6 +65,9 @@ constexpr int64_t kPartBytes = (int64_t)128 << 20;
 constexpr int64_t kGradBytes = (int64_t)512 << 20;
 // fp32 partial sums of dX
 constexpr int64_t kSplitBytes = (int64_t)256 << 20;
+
+// blocks that look for the largest row factor of the backward pass
+constexpr int kPeaks = 255;
 
 // widest piece (a multiple of 256 columns, at least 256) with `per_col` bytes a column within `cap`
 inline int64_t piece(int64_t V, int64_t per_col, int64_t cap) {
@@ -198,7 +200,7 @@ inline Bwd backward(int64_t M, int64_t K, int64_t V, bool pack_w) {
         at += up(n, 256);
         return o;
     };
-    b.off_row = take(16 * M + 64);
+    b.off_row = take(16 * M + 4 * (1 + kPeaks)); // row parameters, the outputs' factor, kPeaks maxima
     b.off_x = take(2 * M * b.Kp);
     b.off_w = take(pack_w ? 2 * K * b.Vc : 0);
     b.off_g = take(2 * M * b.Vc);

@@ -363,48 +363,77 @@ void stats(int rows, bool any, StatsParams &p, hipStream_t s) {
 bool aligned(const void *p, int n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // ---- backward --------------------------------------------------------------------------
-// Row parameters, by the first block, and X's copy (rows that take no part as zeros: theirs
-// may hold anything), by the others.  factor[0] is what both outputs are multiplied by:
-// max |s| (or 1 if that is 0, infinite or NaN), over 2^14 for fp16.
+// Row parameters, by the first `params` blocks, and X's copy (rows that take no part as zeros:
+// theirs may hold anything), by the others.  factor[0] is what both outputs are multiplied
+// by: max |s| (or 1 if that is 0, infinite or NaN), over 2^14 for fp16.  Without row_scale
+// that is every row's |s|; with it each of the `params` blocks takes the maximum itself, over
+// the rows up to kPeakRows, else over k_xent_peak's blocks (with one block for all rows the
+// backward pass at M = 65536, K = 256, V = 1024 took 580 us in place of 399).
 struct PrepParams {
     const int64_t *target;
     const float *lse, *row_scale, *d_scale;
     float scale;
     int64_t M, K, V, Kp;
-    int f16;
+    int f16, params, peaks; // peaks: 0, or the number of entries of `peak`
     RowParam *row;
     float *factor;
+    float *peak; // [xent::kPeaks]
     const uint16_t *X;
     uint16_t *x;
-};
 
-__global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
-    __shared__ float sh[256];
-    const float base = p.scale * (p.d_scale ? p.d_scale[0] : 1.0f);
-    auto s_of = [&](int64_t i) { return p.row_scale ? base * p.row_scale[i] : base; };
-    if (blockIdx.x > 0) {
-        pack_rows(p.X, p.K, p.M, p.K, p.x, p.Kp, (int64_t)(blockIdx.x - 1) * 256 + threadIdx.x,
-                  (int64_t)(gridDim.x - 1) * 256, [&](int64_t r) { return p.target[r] >= 0 && s_of(r) != 0.0f; });
-        return;
-    }
+    __device__ __forceinline__ float base() const { return scale * (d_scale ? d_scale[0] : 1.0f); }
+};
+constexpr int64_t kPeakRows = 1024;
+
+__device__ __forceinline__ float block_max(float v, float (&sh)[4]) {
+#pragma unroll
+    for (int h = 32; h > 0; h >>= 1)
+        v = fmaxf(v, __shfl_xor(v, h, 64));
+    if ((threadIdx.x & 63) == 0)
+        sh[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return fmaxf(fmaxf(sh[0], sh[1]), fmaxf(sh[2], sh[3]));
+}
+
+// largest |s| of the rows that take part, each block over a share of them
+__global__ __launch_bounds__(256) void k_xent_peak(PrepParams p) {
+    __shared__ float sh[4];
+    const float base = p.base();
     float mx = 0.0f;
 #pragma unroll 4
-    for (int64_t i = threadIdx.x; i < p.M; i += 256)
-        if (p.target[i] >= 0)
-            mx = fmaxf(mx, fabsf(s_of(i)));
-    sh[threadIdx.x] = mx;
-    __syncthreads();
-    for (int h = 128; h > 0; h >>= 1) {
-        if ((int)threadIdx.x < h)
-            sh[threadIdx.x] = fmaxf(sh[threadIdx.x], sh[threadIdx.x + h]);
-        __syncthreads();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M; i += (int64_t)gridDim.x * 256)
+        mx = fmaxf(mx, p.target[i] >= 0 ? fabsf(base * p.row_scale[i]) : 0.0f);
+    mx = block_max(mx, sh);
+    if (threadIdx.x == 0)
+        p.peak[blockIdx.x] = mx;
+}
+
+__global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
+    __shared__ float sh[4];
+    const float base = p.base();
+    auto s_of = [&](int64_t i) { return p.row_scale ? base * p.row_scale[i] : base; };
+    if ((int)blockIdx.x >= p.params) {
+        pack_rows(p.X, p.K, p.M, p.K, p.x, p.Kp, (int64_t)(blockIdx.x - p.params) * 256 + threadIdx.x,
+                  (int64_t)(gridDim.x - p.params) * 256, [&](int64_t r) { return p.target[r] >= 0 && s_of(r) != 0.0f; });
+        return;
+    }
+    float mx = fabsf(base);
+    if (p.row_scale) {
+        mx = 0.0f;
+        if (p.peaks) {
+            if ((int)threadIdx.x < p.peaks)
+                mx = p.peak[threadIdx.x];
+        } else {
+            for (int64_t i = threadIdx.x; i < p.M; i += 256)
+                mx = fmaxf(mx, p.target[i] >= 0 ? fabsf(s_of(i)) : 0.0f);
+        }
+        mx = block_max(mx, sh);
     }
     const float unit = p.f16 ? 16384.0f : 1.0f;
-    mx = sh[0] > 0.0f && sh[0] < INFINITY ? sh[0] : 1.0f;
-    if (threadIdx.x == 0)
+    mx = mx > 0.0f && mx < INFINITY ? mx : 1.0f;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
         p.factor[0] = mx / unit;
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < p.M; i += 256) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M; i += (int64_t)p.params * 256) {
         const int64_t t = p.target[i];
         const float s = s_of(i);
         RowParam r{0.0f, 0.0f, -1, 0}; // takes no part
@@ -675,10 +704,15 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
     float *const factor = reinterpret_cast<float *>(ws + b.off_row + 16 * a.M);
     uint16_t *const x = reinterpret_cast<uint16_t *>(ws + b.off_x);
     uint16_t *const wp = reinterpret_cast<uint16_t *>(ws + b.off_w);
-    PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16, row, factor,
+    PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16,
+                  (int)std::min<int64_t>(cdiv(a.M, 256), xent::kCUs), 0, row, factor, factor + 1,
                   static_cast<const uint16_t *>(a.X), x};
+    if (a.row_scale && a.M > kPeakRows) {
+        pp.peaks = (int)std::min<int64_t>(cdiv(a.M, 1024), xent::kPeaks);
+        hipLaunchKernelGGL(k_xent_peak, dim3((unsigned)pp.peaks), dim3(256), 0, s, pp);
+    }
     const int64_t copies = std::min<int64_t>(cdiv(a.M * (b.Kp / 8), 256), 8 * xent::kCUs);
-    hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(1 + copies)), dim3(256), 0, s, pp);
+    hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(pp.params + copies)), dim3(256), 0, s, pp);
     const bool dx_vec = a.K % 4 == 0 && aligned(a.dX, 8);
     for (int64_t v0 = 0; v0 < a.V; v0 += b.Vc) {
         const int64_t vc = std::min(b.Vc, a.V - v0);
