@@ -382,6 +382,22 @@ struct PrepParams {
     uint16_t *x;
 
     __device__ __forceinline__ float base() const { return scale * (d_scale ? d_scale[0] : 1.0f); }
+    // the copy of X by n blocks, of which this is b
+    __device__ __forceinline__ void copy(int b, int n, float base_) const {
+        pack_rows(X, K, M, K, x, Kp, (int64_t)b * 256 + threadIdx.x, (int64_t)n * 256, [&](int64_t r) {
+            return target[r] >= 0 && (row_scale ? base_ * row_scale[r] : base_) != 0.0f;
+        });
+    }
+    // what the rows' s are divided by, from the largest of them
+    static __device__ __forceinline__ float unit_of(float mx) { return mx > 0.0f && mx < INFINITY ? mx : 1.0f; }
+    __device__ __forceinline__ float up() const { return f16 ? 16384.0f : 1.0f; }
+    __device__ __forceinline__ RowParam param(int64_t t, float lse_, float s, float mx) const {
+        if (t >= V)
+            return RowParam{0.0f, NAN, -1, 0}; // no such class: the gradients say so
+        if (t >= 0 && s != 0.0f)
+            return RowParam{lse_ * kLog2e, s / mx * up(), (int)t, 0};
+        return RowParam{0.0f, 0.0f, -1, 0}; // takes no part
+    }
 };
 constexpr int64_t kPeakRows = 1024;
 
@@ -413,8 +429,7 @@ __global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
     const float base = p.base();
     auto s_of = [&](int64_t i) { return p.row_scale ? base * p.row_scale[i] : base; };
     if ((int)blockIdx.x >= p.params) {
-        pack_rows(p.X, p.K, p.M, p.K, p.x, p.Kp, (int64_t)(blockIdx.x - p.params) * 256 + threadIdx.x,
-                  (int64_t)(gridDim.x - p.params) * 256, [&](int64_t r) { return p.target[r] >= 0 && s_of(r) != 0.0f; });
+        p.copy(blockIdx.x - p.params, gridDim.x - p.params, base);
         return;
     }
     float mx = fabsf(base);
@@ -429,20 +444,11 @@ __global__ __launch_bounds__(256) void k_xent_prep(PrepParams p) {
         }
         mx = block_max(mx, sh);
     }
-    const float unit = p.f16 ? 16384.0f : 1.0f;
-    mx = mx > 0.0f && mx < INFINITY ? mx : 1.0f;
+    mx = PrepParams::unit_of(mx);
     if (blockIdx.x == 0 && threadIdx.x == 0)
-        p.factor[0] = mx / unit;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M; i += (int64_t)p.params * 256) {
-        const int64_t t = p.target[i];
-        const float s = s_of(i);
-        RowParam r{0.0f, 0.0f, -1, 0}; // takes no part
-        if (t >= p.V)
-            r = RowParam{0.0f, NAN, -1, 0}; // no such class: the gradients say so
-        else if (t >= 0 && s != 0.0f)
-            r = RowParam{p.lse[i] * kLog2e, s / mx * unit, (int)t, 0};
-        p.row[i] = r;
-    }
+        p.factor[0] = mx / p.up();
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < p.M; i += (int64_t)p.params * 256)
+        p.row[i] = p.param(p.target[i], p.lse[i], s_of(i), mx);
 }
 
 struct GradParams {
@@ -450,28 +456,64 @@ struct GradParams {
     const RowParam *row;
     int64_t v0, Vg; // first column of the piece; columns of G (a multiple of 64, zero past J)
     uint16_t *g;    // [M, Vg]
+    PrepParams prep; // OWN
+    int tiles;       // OWN: blocks of tiles; the others copy X
 };
 
+// OWN, up to 64 rows, saves the launch that prepares them (40.6 -> 37.9 us at M = 16, K = 1024,
+// V = 32000): each wave takes its rows' parameters and the largest |s| from the arrays
+// while its first operands are on their way, X is read as it is (a row out of the loss is
+// dropped by its s), and blocks behind the tiles make the copy that dW needs.
 // The piece of G = (exp(z − lse) − onehot)·s; the row parameters are loaded once the sums
 // stand, 16 bytes a row and lane, and G leaves through LDS in whole lines (M = 8192,
 // K = 4096, a piece of 32768 columns: 1.62 ms, 1.36 PFLOP/s).
-template <class C>
+template <class C, bool OWN>
 __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(GradParams p) {
     __shared__ __attribute__((aligned(1024))) char smem_raw[C::kLds];
     LB_LDS char *smem = (LB_LDS char *)smem_raw;
-    int ti, tj;
-    coords(p.job, gathered(blockIdx.x, gridDim.x), ti, tj);
-    Acc<C> acc;
-    accumulate<C>(p.job, ti, tj, smem, acc);
     const int lane = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int ti, tj;
+    if constexpr (OWN) {
+        if ((int)blockIdx.x >= p.tiles) {
+            p.prep.copy(blockIdx.x - p.tiles, gridDim.x - p.tiles, p.prep.base());
+            return;
+        }
+        coords(p.job, gathered(blockIdx.x, p.tiles), ti, tj);
+    } else {
+        coords(p.job, gathered(blockIdx.x, gridDim.x), ti, tj);
+    }
     const int64_t ib = (int64_t)ti * C::TI + (w / C::WJ) * C::FI * 16;
     const int64_t jb = (int64_t)tj * C::TJ + (w % C::WJ) * C::FJ * 16;
     RowParam rp[C::FI];
+    if constexpr (OWN) {
+        const PrepParams &q = p.prep;
+        const float base = q.base();
+        auto s_of = [&](int64_t i) { return q.row_scale ? base * q.row_scale[i] : base; };
+        float mx = fabsf(base);
+        if (q.row_scale) { // M <= 64: a row a lane
+            mx = lane < q.M && q.target[lane] >= 0 ? fmaxf(0.0f, fabsf(s_of(lane))) : 0.0f;
 #pragma unroll
-    for (int x = 0; x < C::FI; ++x) {
-        const int64_t i = ib + 16 * x + (lane & 15);
-        rp[x] = i < p.job.I ? p.row[i] : RowParam{0.0f, 0.0f, -1, 0};
+            for (int h = 32; h > 0; h >>= 1)
+                mx = fmaxf(mx, __shfl_xor(mx, h, 64));
+        }
+        mx = PrepParams::unit_of(mx);
+        if (blockIdx.x == 0 && threadIdx.x == 0)
+            q.factor[0] = mx / q.up();
+#pragma unroll
+        for (int x = 0; x < C::FI; ++x) {
+            const int64_t i = ib + 16 * x + (lane & 15);
+            rp[x] = i < q.M ? q.param(q.target[i], q.lse[i], s_of(i), mx) : RowParam{0.0f, 0.0f, -1, 0};
+        }
+    }
+    Acc<C> acc;
+    accumulate<C>(p.job, ti, tj, smem, acc);
+    if constexpr (!OWN) {
+#pragma unroll
+        for (int x = 0; x < C::FI; ++x) {
+            const int64_t i = ib + 16 * x + (lane & 15);
+            rp[x] = i < p.job.I ? p.row[i] : RowParam{0.0f, 0.0f, -1, 0};
+        }
     }
     const int j0 = (int)jb + 4 * (lane >> 4);
     store16<C>(acc, p.g, p.Vg, p.job.I, p.Vg, ib, jb, true, false, smem, [](int) {}, [&](int x, int y) {
@@ -482,7 +524,7 @@ __global__ __launch_bounds__(kThreads, C::TI == 256 ? 1 : 2) void k_xent_grad(Gr
             const int j = j0 + 16 * y + e;
             const float pr = exp2_fast(__builtin_fmaf(acc[x][y][e], kLog2e, -rp[x].lse2));
             g[e] = (j == t ? pr - 1.0f : pr) * rp[x].s;
-            g[e] = j < (int)p.job.J ? g[e] : 0.0f;
+            g[e] = j < (int)p.job.J && !(OWN && rp[x].s == 0.0f) ? g[e] : 0.0f;
         }
         return u32x2_t{C::T::pack2(g[0], g[1]), C::T::pack2(g[2], g[3])};
     });
@@ -661,7 +703,16 @@ void run_grad(GradParams &g, hipStream_t s) {
     set_tiles<C>(g.job);
     // G's padding columns (up to a multiple of 64) are zeroed by the tiles that own them
     g.job.tiles_j = (int)cdiv(g.Vg, C::TJ);
-    hipLaunchKernelGGL((k_xent_grad<C>), dim3((unsigned)(g.job.tiles_i * g.job.tiles_j)), dim3(kThreads), 0, s, g);
+    const int tiles = g.job.tiles_i * g.job.tiles_j;
+    if constexpr (C::TI <= 64) {
+        if (g.tiles) { // OWN: up to a block per CU copies X
+            g.tiles = tiles;
+            const int64_t copies = std::min<int64_t>(cdiv(g.prep.M * (g.prep.Kp / 8), 256), xent::kCUs);
+            hipLaunchKernelGGL((k_xent_grad<C, true>), dim3((unsigned)(tiles + copies)), dim3(kThreads), 0, s, g);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_xent_grad<C, false>), dim3((unsigned)tiles), dim3(kThreads), 0, s, g);
 }
 template <class T>
 void grad(int rows, bool any, GradParams &g, hipStream_t s) {
@@ -707,12 +758,15 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
     PrepParams pp{a.target, a.lse, a.row_scale, a.d_scale, a.scale, a.M, a.K, a.V, b.Kp, a.f16,
                   (int)std::min<int64_t>(cdiv(a.M, 256), xent::kCUs), 0, row, factor, factor + 1,
                   static_cast<const uint16_t *>(a.X), x};
+    // the logits' kernel prepares the rows itself
+    const bool own = a.M <= 64 && b.rows <= xent::ROWS64 && b.Vc >= a.V && a.K % 8 == 0 && aligned(a.X, 16);
     if (a.row_scale && a.M > kPeakRows) {
         pp.peaks = (int)std::min<int64_t>(cdiv(a.M, 1024), xent::kPeaks);
         hipLaunchKernelGGL(k_xent_peak, dim3((unsigned)pp.peaks), dim3(256), 0, s, pp);
     }
     const int64_t copies = std::min<int64_t>(cdiv(a.M * (b.Kp / 8), 256), 8 * xent::kCUs);
-    hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(pp.params + copies)), dim3(256), 0, s, pp);
+    if (!own)
+        hipLaunchKernelGGL(k_xent_prep, dim3((unsigned)(pp.params + copies)), dim3(256), 0, s, pp);
     const bool dx_vec = a.K % 4 == 0 && aligned(a.dX, 8);
     for (int64_t v0 = 0; v0 < a.V; v0 += b.Vc) {
         const int64_t vc = std::min(b.Vc, a.V - v0);
@@ -724,8 +778,10 @@ hipError_t backward(const XentBwdArgs &a, hipStream_t s) {
             ldw = b.Vc;
         }
         GradParams g{};
-        g.job.a = x;
-        g.job.lda = b.Kp;
+        g.job.a = own ? static_cast<const uint16_t *>(a.X) : x;
+        g.job.lda = own ? a.K : b.Kp;
+        g.prep = pp;
+        g.tiles = own;
         g.job.b = w;
         g.job.ldb = ldw;
         g.job.I = a.M;

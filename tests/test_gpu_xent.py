@@ -457,9 +457,9 @@ def test_loss_of_a_nearly_sure_row(M, V, dtype):
     assert bool(((lse.double() - 1000.0 - ref).abs() <= 4 * U * 1000 + bound).all())
 
 
-@pytest.mark.parametrize("M", [900, 5000])
+@pytest.mark.parametrize("M", [50, 900, 5000])
 def test_row_weights_of_many_rows(M):
-    """The largest |s| from the rows themselves and from a launch of its own; weights of rows out
+    """The largest |s| from a wave, from the rows themselves and from a launch of its own; weights of rows out
     of the loss may hold anything."""
     X, W, t = case(M, 40, 300, "f16", seed=9)
     w = torch.rand(M, device=DEV) * 2e-5
